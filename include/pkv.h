@@ -77,7 +77,7 @@ typedef enum {
   PKV_ERR_OUT_OF_PAGES = 7   /* allocator: not enough free pages (nothing was changed) */
 } pkv_status;
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
+typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_I8 = 2, PKV_E4M3 = 3 } pkv_dtype;
 
 /* Device error bits, as returned in *bits by pkv_last_device_error(). */
 #define PKV_DEVERR_BAD_PAGE 0x1u   /* block_table entry outside [0, num_pages): its keys left out */
@@ -302,6 +302,162 @@ PKV_API int paged_kv_copy_pages(void* k_pages, void* v_pages, const int32_t* src
                                 const int32_t* dst, int n, int num_pages, int page_size,
                                 int H_kv, int d, int dtype, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* The 8-bit cache.                                                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Pages hold codes, k_pages and v_pages [num_pages, page_size, H_kv, d] bytes,
+ * and every block of block_tokens tokens of a page has one float32 scale for
+ * each kv head, k_scales and v_scales [num_pages, page_size / block_tokens, H_kv]:
+ *
+ *     K[token t][head h][c] = code[t][h][c] * k_scales[page][offset / block_tokens][h]
+ *
+ * cache_dtype  : PKV_I8 (two's complement codes -127 .. 127) or PKV_E4M3 (1 sign,
+ *                4 exponent bits with bias 7, 3 mantissa bits, largest 448).
+ * block_tokens : a power of two in [16, page_size].
+ * d            : 128.
+ */
+
+/*
+ * paged_kv_append_q8 - quantise new tokens' K and V rows into their pages.
+ *
+ * For each block of a page that the call writes into, and each kv head, K and V
+ * apart, with amax the largest magnitude among the call's new rows of the block:
+ *
+ *     s_new          = max(s_old, amax / qmax, 2^-126)    qmax = 127 or 448
+ *     code(new row)  = nearest(x / s_new)
+ *     code(old row)  = nearest(code * s_old / s_new)      where s_new > s_old
+ *
+ * nearest() rounds the exact quotient, ties to even.  s_old is 0 where the call
+ * writes the block's first token (a reused page needs no clearing), else the
+ * block's scale so far, and its old rows are those before the call's first.  So
+ * no value is ever clipped, and codes change only where a scale grows.  A block
+ * that takes in a NaN or an infinity gets scale NaN and codes 0, and stays NaN
+ * until its first token is written anew: attention over it gives NaN, as over
+ * the values themselves.
+ *
+ * k_new, v_new, cu_new, start_pos, block_table, num_new, num_seqs and the pool's
+ * sizes mean what they mean in paged_kv_append.  dtype is the new rows' type,
+ * PKV_BF16 or PKV_F32.  Rows of two sequences must not fall into one block in
+ * one call.  Rows whose page is outside the pool or past the table are skipped
+ * and flagged.  Returns PKV_OK without reading any pointer when num_new == 0.
+ */
+PKV_API int paged_kv_append_q8(const void* k_new, const void* v_new, const int32_t* cu_new,
+                               const int32_t* start_pos, const int32_t* block_table,
+                               int max_pages_per_seq, int num_seqs, int num_new, void* k_pages,
+                               void* v_pages, void* k_scales, void* v_scales, int num_pages,
+                               int page_size, int block_tokens, int H_kv, int d, int dtype,
+                               int cache_dtype, void* stream);
+
+/*
+ * paged_kv_copy_pages_q8 - copy whole pages (codes and scales, K and V): page
+ * src[i] -> page dst[i], as paged_kv_copy_pages does for the other caches.
+ */
+PKV_API int paged_kv_copy_pages_q8(void* k_pages, void* v_pages, void* k_scales, void* v_scales,
+                                   const int32_t* src, const int32_t* dst, int n, int num_pages,
+                                   int page_size, int block_tokens, int H_kv, int d,
+                                   int cache_dtype, void* stream);
+
+/*
+ * paged_attn_q8 - attention of new query tokens against an 8-bit paged cache.
+ *
+ * What paged_attn computes with K and V the values the codes stand for; q and
+ * out are PKV_BF16.  Arguments that both have mean the same (the page table, the
+ * lengths, q_len == 1 for decode, causal, the rules for bad pages and lengths).
+ * workspace : device scratch of >= paged_attn_q8_workspace_size() bytes, 256-byte
+ *             aligned (NULL if that size is 0), one for each call in flight.
+ */
+PKV_API size_t paged_attn_q8_workspace_size(int num_seqs, int q_len, int H, int H_kv,
+                                            int max_seq_len, int page_size);
+PKV_API int paged_attn_q8(const void* q, const void* k_pages, const void* v_pages,
+                          const void* k_scales, const void* v_scales, const int32_t* block_table,
+                          const int32_t* seq_lens, int page_size, int block_tokens, int num_seqs,
+                          int q_len, int H, int H_kv, int d, int num_pages, int max_pages_per_seq,
+                          int max_seq_len, int causal, float scale, int cache_dtype, void* out,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention weights, and eviction by them.                                 */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * paged_attn_weights - attention that also accumulates how much weight each
+ * key received.
+ *
+ * out is what paged_attn (cache_dtype PKV_BF16) or paged_attn_q8 (PKV_I8,
+ * PKV_E4M3) computes, and for every sequence s, kv head k and visible key j
+ *
+ *     weights[s][k][j] += sum over the query heads h of k, and the q_len rows i,
+ *                         of P[s][h][i][j],   P = softmax(Q K^T * scale)
+ *
+ * in float32.  Keys of a page outside the pool get nothing, and entries from a
+ * sequence's length on are neither read nor written.  The sums have a fixed
+ * order: the same call gives the same bits.
+ *
+ * k_scales, v_scales, block_tokens : as in paged_attn_q8; not looked at when
+ *             cache_dtype is PKV_BF16.
+ * weights   : device float32 [num_seqs, H_kv, weights_stride], added to.
+ * weights_stride : >= max_seq_len.
+ * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.
+ * H / H_kv is at most 256.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
+ */
+PKV_API size_t paged_attn_weights_workspace_size(int num_seqs, int q_len, int H, int H_kv,
+                                                 int max_seq_len, int page_size);
+PKV_API int paged_attn_weights(const void* q, const void* k_pages, const void* v_pages,
+                               const void* k_scales, const void* v_scales,
+                               const int32_t* block_table, const int32_t* seq_lens, int page_size,
+                               int block_tokens, int num_seqs, int q_len, int H, int H_kv, int d,
+                               int num_pages, int max_pages_per_seq, int max_seq_len, int causal,
+                               float scale, int cache_dtype, void* out, void* weights,
+                               int weights_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * paged_kv_evict - shorten every sequence to `budget` tokens.
+ *
+ * A sequence of L tokens keeps m = min(L, budget).  Each kv head keeps, of its
+ * own, the last min(recent, L) tokens and, of the others, the ones with the
+ * largest weights (equal weights: the lowest index; a NaN counts as smaller
+ * than any number).  Kept tokens keep their order and become tokens 0 .. m - 1
+ * through dst_table.  Heads of one sequence may keep different tokens: what is
+ * stored at a token's slot of head h belongs to token kept[s][h][slot].
+ *
+ * weights     : device float32 [num_seqs, H_kv, weights_stride], as
+ *               paged_attn_weights accumulates them.
+ * weights_out : the kept tokens' weights go to entries 0 .. m - 1 and zero to
+ *               m .. L - 1; the rest is left alone.  May be `weights` itself.
+ * block_table : where the tokens are; dst_table: where they go, same shape.  A
+ *               page of dst_table is either the one that block_table has at
+ *               that place (compaction in place; the two tables may be the same
+ *               array) or a page that no sequence of the call reads or writes
+ *               otherwise.  A page that several sequences of the call read is
+ *               a destination of none (pkv_alloc_compact sees to all this).
+ * seq_lens    : lengths before; new_lens: lengths after (another array).
+ * kept        : device int32 [num_seqs, H_kv, budget]: the kept tokens' old
+ *               indices, ascending, -1 from m on.
+ * budget      : >= 1; recent: in [0, budget].
+ * cache_dtype : PKV_BF16 or PKV_F32 (d 64 or 128; k_scales, v_scales and
+ *               block_tokens are not looked at), PKV_I8 or PKV_E4M3 (d 128).
+ *               An 8-bit block's new scale is the largest of its rows' scales,
+ *               and a row of another scale gets nearest(code * s_old / s_new);
+ *               a NaN scale makes the block NaN with codes 0.
+ * workspace   : >= paged_kv_evict_workspace_size() bytes, 256-byte aligned (NULL
+ *               if that size is 0), one for each call in flight.
+ * A token whose page is outside the pool is not moved, and a length outside its
+ * table is clamped; both are flagged.
+ */
+PKV_API size_t paged_kv_evict_workspace_size(int num_seqs, int H_kv, int budget, int block_tokens,
+                                             int cache_dtype);
+PKV_API int paged_kv_evict(void* k_pages, void* v_pages, void* k_scales, void* v_scales,
+                           const void* weights, void* weights_out, int weights_stride,
+                           const int32_t* block_table, const int32_t* dst_table,
+                           const int32_t* seq_lens, int32_t* new_lens, int32_t* kept, int budget,
+                           int recent, int num_seqs, int H_kv, int d, int num_pages,
+                           int page_size, int block_tokens, int max_pages_per_seq,
+                           int max_seq_len, int cache_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /*
  * pkv_alloc_* - host page allocator (bookkeeping only; host memory).
  *
@@ -325,6 +481,17 @@ PKV_API int paged_kv_copy_pages(void* k_pages, void* v_pages, const int32_t* src
  *                       *cow_dst with *n_cow = 1 (else *n_cow = 0).
  *                       PKV_ERR_OUT_OF_PAGES leaves everything unchanged.
  * pkv_alloc_fork      : child_id shares all of parent_id's pages (same length).
+ * pkv_alloc_compact   : make the n listed sequences (each once) new_lens[i]
+ *                       tokens long (0 <= new_lens[i] <= their length), as
+ *                       paged_kv_evict leaves them: of the pages a sequence
+ *                       still needs, those that others share are replaced by
+ *                       fresh ones, and the pages past them are given up.  The
+ *                       tables before the call are paged_kv_evict's block_table,
+ *                       those after it its dst_table; pages given up must not be
+ *                       written before that call has run (later calls on its
+ *                       stream are late enough).  List all sequences of one
+ *                       paged_kv_evict call in one call.  PKV_ERR_OUT_OF_PAGES
+ *                       leaves everything unchanged.
  * pkv_alloc_free_seq  : drop seq_id; pages nobody else holds return to the pool.
  * pkv_alloc_seq_len   : current length of seq_id.
  * pkv_alloc_block_table: host arrays table [n][max_pages_per_seq] (-1 padded)
@@ -339,6 +506,7 @@ PKV_API int pkv_alloc_add_seq(pkv_allocator* a, int seq_id);
 PKV_API int pkv_alloc_reserve(pkv_allocator* a, int seq_id, int n_tokens, int32_t* start_pos,
                               int32_t* cow_src, int32_t* cow_dst, int* n_cow);
 PKV_API int pkv_alloc_fork(pkv_allocator* a, int parent_id, int child_id);
+PKV_API int pkv_alloc_compact(pkv_allocator* a, const int* seq_ids, int n, const int* new_lens);
 PKV_API int pkv_alloc_free_seq(pkv_allocator* a, int seq_id);
 PKV_API int pkv_alloc_seq_len(const pkv_allocator* a, int seq_id, int* len);
 PKV_API int pkv_alloc_block_table(const pkv_allocator* a, const int* seq_ids, int n,

@@ -3,9 +3,20 @@
 Callers that hold torch tensors use these; every step of the computation runs
 in ``libpkv.so``.  Outputs (and the decode workspace, unless one is passed)
 are allocated with torch on the inputs' device.
+
+The cache in 8 bits (``append_q8``, ``copy_pages_q8``, ``paged_q8``) holds its
+codes in int8 or float8_e4m3fn pages and one float32 scale for each block of
+tokens and kv head; ``paged_weights`` and ``evict`` keep a cache within a budget
+of tokens.  These five check their tensors, raise ValueError or TypeError for
+ones that do not fit together, and run on the tensors' device whichever device
+is current.  With ``stream`` None they run on that device's current stream;
+another stream the caller orders against the tensors' producers and consumers
+(what these functions allocate themselves is kept for that stream's work).
 """
 
 from __future__ import annotations
+
+import contextlib
 
 import torch
 
@@ -55,3 +66,174 @@ def paged(q, k_pages, v_pages, block_table, seq_lens, page_size: int, causal: bo
                  P, block_table.shape[1], max_seq_len, causal, scale, _dtype(q), o, ws,
                  ws_bytes, stream)
     return o
+
+
+# ------------------------------------------------ 8-bit cache, weights, eviction --
+
+_Q8 = {torch.int8: B.PKV_I8, torch.float8_e4m3fn: B.PKV_E4M3}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(*tensors):
+    """A context in which the tensors' device is current (nothing to do if it is)."""
+    dev = tensors[0].device
+    for t in tensors:
+        _need(t.is_cuda and t.device == dev, "every tensor must be on one CUDA device")
+        _need(t.is_contiguous(), "every tensor must be contiguous")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _pools(k_pages, v_pages, k_scales, v_scales):
+    """(cache dtype, tokens a block) of a pool of pages and its scales."""
+    _need(k_pages.dim() == 4 and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
+          "k_pages and v_pages must be [pages, page_size, H_kv, d] of one type")
+    if k_pages.dtype in _DT:
+        _need(k_scales is None and v_scales is None, "only an 8-bit cache has scales")
+        return _DT[k_pages.dtype], 0
+    if k_pages.dtype not in _Q8:
+        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+    _need(k_scales is not None and v_scales is not None, "an 8-bit cache needs its scales")
+    P, ps, H_kv, _ = k_pages.shape
+    _need(k_scales.dtype == torch.float32 and v_scales.dtype == torch.float32, "scales must be float32")
+    _need(k_scales.dim() == 3 and v_scales.shape == k_scales.shape and k_scales.shape[0] == P
+          and k_scales.shape[2] == H_kv and k_scales.shape[1] > 0 and ps % k_scales.shape[1] == 0,
+          "scales must be [pages, page_size / block_tokens, H_kv]")
+    return _Q8[k_pages.dtype], ps // k_scales.shape[1]
+
+
+def _int32(*tensors):
+    for t in tensors:
+        _need(t.dtype == torch.int32, "tables, lengths and indices must be int32")
+
+
+def _workspace(workspace, n, device):
+    if workspace is None and n:
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _used_on(stream, *tensors):
+    """Keep what was allocated here from being reused before another stream's work has run."""
+    if stream is not None:
+        st = torch.cuda.ExternalStream(B._stream(stream), device=tensors[0].device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(st)
+
+
+def append_q8(k_new, v_new, cu_new, start_pos, block_table, k_pages, v_pages, k_scales, v_scales,
+              stream=None) -> None:
+    """Quantise new K/V rows [num_new, H_kv, d] (bf16 or f32) into an 8-bit cache, in place."""
+    cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
+    if cache not in (B.PKV_I8, B.PKV_E4M3):
+        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+    P, ps, H_kv, d = k_pages.shape
+    _need(k_new.dim() == 3 and k_new.shape[1:] == (H_kv, d) and v_new.shape == k_new.shape
+          and v_new.dtype == k_new.dtype, "k_new and v_new must be [num_new, H_kv, d] of one type")
+    _int32(cu_new, start_pos, block_table)
+    S = start_pos.numel()
+    _need(cu_new.numel() == S + 1 and block_table.dim() == 2 and block_table.shape[0] == S,
+          "cu_new must hold num_seqs + 1 entries and block_table a row for each sequence")
+    with _on_device(k_pages, v_pages, k_scales, v_scales, k_new, v_new, cu_new, start_pos, block_table):
+        B.paged_kv_append_q8(k_new, v_new, cu_new, start_pos, block_table, block_table.shape[1], S,
+                             k_new.shape[0], k_pages, v_pages, k_scales, v_scales, P, ps, block, H_kv, d,
+                             _dtype(k_new), cache, stream)
+
+
+def copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None) -> None:
+    """Copy pages src[i] -> dst[i] of an 8-bit cache, codes and scales."""
+    cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
+    if cache not in (B.PKV_I8, B.PKV_E4M3):
+        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+    P, ps, H_kv, d = k_pages.shape
+    _int32(src, dst)
+    _need(src.shape == dst.shape, "as many sources as destinations")
+    with _on_device(k_pages, v_pages, k_scales, v_scales, src, dst):
+        B.paged_kv_copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, src.numel(), P, ps, block, H_kv,
+                                 d, cache, stream)
+
+
+def _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out):
+    _need(q.dim() == 4 and q.dtype == torch.bfloat16, "q must be bf16 [num_seqs, H, q_len, d]")
+    S, H, q_len, d = q.shape
+    _, ps, H_kv, d2 = k_pages.shape
+    _need(ps == page_size and d2 == d, "pages must hold page_size tokens of q's head dim")
+    _int32(block_table, seq_lens)
+    _need(block_table.dim() == 2 and block_table.shape[0] == S and seq_lens.numel() == S,
+          "block_table and seq_lens must hold a row and a length for each sequence")
+    o = torch.empty_like(q) if out is None else out
+    _need(o.shape == q.shape and o.dtype == q.dtype, "out must look like q")
+    return S, H, q_len, d, H_kv, o
+
+
+def paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size: int, causal: bool,
+             scale: float, max_seq_len: int, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention over an 8-bit paged cache: q [S, H, q_len, d] bf16; pages [P, page_size, H_kv, d]."""
+    cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
+    if cache not in (B.PKV_I8, B.PKV_E4M3):
+        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+    S, H, q_len, d, H_kv, o = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
+    with _on_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, o):
+        ws, n = _workspace(workspace, B.paged_attn_q8_workspace_size(S, q_len, H, H_kv, max_seq_len, page_size),
+                           q.device)
+        B.paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S, q_len,
+                        H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale, cache, o,
+                        ws, n, stream)
+        _used_on(stream, o, ws)
+    return o
+
+
+def paged_weights(q, k_pages, v_pages, block_table, seq_lens, page_size: int, causal: bool, scale: float,
+                  max_seq_len: int, weights, k_scales=None, v_scales=None, out=None, workspace=None,
+                  stream=None) -> torch.Tensor:
+    """Attention over a bf16 or 8-bit paged cache that adds every key's softmax weight, summed over the
+    query rows and the query heads of its kv head, to ``weights`` [S, H_kv, >= max_seq_len] (float32)."""
+    cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
+    S, H, q_len, d, H_kv, o = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
+    _need(weights.dtype == torch.float32 and weights.dim() == 3 and weights.shape[:2] == (S, H_kv)
+          and weights.shape[2] >= max_seq_len, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
+    more = () if block == 0 else (k_scales, v_scales)
+    with _on_device(q, k_pages, v_pages, block_table, seq_lens, o, weights, *more):
+        ws, n = _workspace(workspace, B.paged_attn_weights_workspace_size(S, q_len, H, H_kv, max_seq_len, page_size),
+                           q.device)
+        B.paged_attn_weights(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S,
+                             q_len, H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale,
+                             cache, o, weights, weights.shape[2], ws, n, stream)
+        _used_on(stream, o, ws)
+    return o
+
+
+def evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, recent: int, max_seq_len: int,
+          dst_table=None, weights_out=None, k_scales=None, v_scales=None, workspace=None, stream=None):
+    """Shorten every sequence to ``budget`` tokens: the last ``recent`` ones and those of the largest weight.
+
+    Compacts K, V and (into ``weights_out``, default ``weights`` itself) the weights; ``dst_table`` (default
+    ``block_table``: in place) says where kept tokens go.  Returns (kept [S, H_kv, budget] int32: their old
+    indices, -1 padded; the new lengths [S] int32)."""
+    cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
+    P, ps, H_kv, d = k_pages.shape
+    dst_table = block_table if dst_table is None else dst_table
+    weights_out = weights if weights_out is None else weights_out
+    _int32(block_table, dst_table, seq_lens)
+    S = seq_lens.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == S and dst_table.shape == block_table.shape,
+          "block_table and dst_table must hold a row for each sequence")
+    _need(weights.dtype == torch.float32 and weights.dim() == 3 and weights.shape[:2] == (S, H_kv)
+          and weights.shape[2] >= max_seq_len and weights_out.shape == weights.shape
+          and weights_out.dtype == torch.float32, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
+    more = () if block == 0 else (k_scales, v_scales)
+    with _on_device(k_pages, v_pages, weights, weights_out, block_table, dst_table, seq_lens, *more):
+        kept = torch.empty((S, H_kv, max(budget, 0)), dtype=torch.int32, device=k_pages.device)
+        new_lens = torch.empty_like(seq_lens)
+        ws, n = _workspace(workspace, B.paged_kv_evict_workspace_size(S, H_kv, budget, block, cache), k_pages.device)
+        B.paged_kv_evict(k_pages, v_pages, k_scales, v_scales, weights, weights_out, weights.shape[2], block_table,
+                         dst_table, seq_lens, new_lens, kept, budget, recent, S, H_kv, d, P, ps, block,
+                         block_table.shape[1], max_seq_len, cache, ws, n, stream)
+        _used_on(stream, kept, new_lens, ws)
+    return kept, new_lens

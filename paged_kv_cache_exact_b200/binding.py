@@ -28,7 +28,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA = 0, 1, 2, 3
 PKV_ERR_TIMEOUT, PKV_ERR_BAD_TABLE, PKV_ERR_WORKSPACE, PKV_ERR_OUT_OF_PAGES = 4, 5, 6, 7
-PKV_F32, PKV_BF16 = 0, 1
+PKV_F32, PKV_BF16, PKV_I8, PKV_E4M3 = 0, 1, 2, 3
 PKV_DEVERR_BAD_PAGE, PKV_DEVERR_BAD_LEN, PKV_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 PKV_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -53,6 +53,22 @@ _lib.paged_kv_append.restype = _i
 _lib.paged_kv_append.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp]
 _lib.paged_kv_copy_pages.restype = _i
 _lib.paged_kv_copy_pages.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
+_lib.paged_kv_append_q8.restype = _i
+_lib.paged_kv_append_q8.argtypes = [_vp] * 5 + [_i] * 3 + [_vp] * 4 + [_i] * 7 + [_vp]
+_lib.paged_kv_copy_pages_q8.restype = _i
+_lib.paged_kv_copy_pages_q8.argtypes = [_vp] * 6 + [_i] * 7 + [_vp]
+_lib.paged_attn_q8_workspace_size.restype = _sz
+_lib.paged_attn_q8_workspace_size.argtypes = [_i] * 6
+_lib.paged_attn_q8.restype = _i
+_lib.paged_attn_q8.argtypes = [_vp] * 7 + [_i] * 11 + [_f, _i, _vp, _vp, _sz, _vp]
+_lib.paged_attn_weights_workspace_size.restype = _sz
+_lib.paged_attn_weights_workspace_size.argtypes = [_i] * 6
+_lib.paged_attn_weights.restype = _i
+_lib.paged_attn_weights.argtypes = [_vp] * 7 + [_i] * 11 + [_f, _i, _vp, _vp, _i, _vp, _sz, _vp]
+_lib.paged_kv_evict_workspace_size.restype = _sz
+_lib.paged_kv_evict_workspace_size.argtypes = [_i] * 5
+_lib.paged_kv_evict.restype = _i
+_lib.paged_kv_evict.argtypes = [_vp] * 6 + [_i] + [_vp] * 5 + [_i] * 11 + [_vp, _sz, _vp]
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _lib.pkv_alloc_create.restype = _vp
 _lib.pkv_alloc_create.argtypes = [_i, _i, _i]
@@ -64,6 +80,8 @@ _lib.pkv_alloc_reserve.restype = _i
 _lib.pkv_alloc_reserve.argtypes = [_vp, _i, _i, _i32p, _i32p, _i32p, ctypes.POINTER(_i)]
 _lib.pkv_alloc_fork.restype = _i
 _lib.pkv_alloc_fork.argtypes = [_vp, _i, _i]
+_lib.pkv_alloc_compact.restype = _i
+_lib.pkv_alloc_compact.argtypes = [_vp, ctypes.POINTER(_i), _i, ctypes.POINTER(_i)]
 _lib.pkv_alloc_free_seq.restype = _i
 _lib.pkv_alloc_free_seq.argtypes = [_vp, _i]
 _lib.pkv_alloc_seq_len.restype = _i
@@ -172,6 +190,69 @@ def paged_kv_copy_pages(k_pages, v_pages, src, dst, n, num_pages, page_size, H_k
         dtype, _stream(stream)))
 
 
+def paged_kv_append_q8(k_new, v_new, cu_new, start_pos, block_table, max_pages_per_seq, num_seqs,
+                       num_new, k_pages, v_pages, k_scales, v_scales, num_pages, page_size,
+                       block_tokens, H_kv, d, dtype, cache_dtype, stream=None):
+    _check("paged_kv_append_q8", _lib.paged_kv_append_q8(
+        _ptr(k_new), _ptr(v_new), _ptr(cu_new), _ptr(start_pos), _ptr(block_table),
+        max_pages_per_seq, num_seqs, num_new, _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
+        _ptr(v_scales), num_pages, page_size, block_tokens, H_kv, d, dtype, cache_dtype,
+        _stream(stream)))
+
+
+def paged_kv_copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, n, num_pages, page_size,
+                           block_tokens, H_kv, d, cache_dtype, stream=None):
+    _check("paged_kv_copy_pages_q8", _lib.paged_kv_copy_pages_q8(
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(src), _ptr(dst), n,
+        num_pages, page_size, block_tokens, H_kv, d, cache_dtype, _stream(stream)))
+
+
+def paged_attn_q8_workspace_size(num_seqs, q_len, H, H_kv, max_seq_len, page_size) -> int:
+    return _lib.paged_attn_q8_workspace_size(num_seqs, q_len, H, H_kv, max_seq_len, page_size)
+
+
+def paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size,
+                  block_tokens, num_seqs, q_len, H, H_kv, d, num_pages, max_pages_per_seq,
+                  max_seq_len, causal, scale, cache_dtype, out, workspace, workspace_bytes,
+                  stream=None):
+    _check("paged_attn_q8", _lib.paged_attn_q8(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+        _ptr(seq_lens), page_size, block_tokens, num_seqs, q_len, H, H_kv, d, num_pages,
+        max_pages_per_seq, max_seq_len, int(causal), float(scale), cache_dtype, _ptr(out),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def paged_attn_weights_workspace_size(num_seqs, q_len, H, H_kv, max_seq_len, page_size) -> int:
+    return _lib.paged_attn_weights_workspace_size(num_seqs, q_len, H, H_kv, max_seq_len, page_size)
+
+
+def paged_attn_weights(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size,
+                       block_tokens, num_seqs, q_len, H, H_kv, d, num_pages, max_pages_per_seq,
+                       max_seq_len, causal, scale, cache_dtype, out, weights, weights_stride,
+                       workspace, workspace_bytes, stream=None):
+    _check("paged_attn_weights", _lib.paged_attn_weights(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+        _ptr(seq_lens), page_size, block_tokens, num_seqs, q_len, H, H_kv, d, num_pages,
+        max_pages_per_seq, max_seq_len, int(causal), float(scale), cache_dtype, _ptr(out),
+        _ptr(weights), weights_stride, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def paged_kv_evict_workspace_size(num_seqs, H_kv, budget, block_tokens, cache_dtype) -> int:
+    return _lib.paged_kv_evict_workspace_size(num_seqs, H_kv, budget, block_tokens, cache_dtype)
+
+
+def paged_kv_evict(k_pages, v_pages, k_scales, v_scales, weights, weights_out, weights_stride,
+                   block_table, dst_table, seq_lens, new_lens, kept, budget, recent, num_seqs, H_kv,
+                   d, num_pages, page_size, block_tokens, max_pages_per_seq, max_seq_len,
+                   cache_dtype, workspace, workspace_bytes, stream=None):
+    _check("paged_kv_evict", _lib.paged_kv_evict(
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(weights),
+        _ptr(weights_out), weights_stride, _ptr(block_table), _ptr(dst_table), _ptr(seq_lens),
+        _ptr(new_lens), _ptr(kept), budget, recent, num_seqs, H_kv, d, num_pages, page_size,
+        block_tokens, max_pages_per_seq, max_seq_len, cache_dtype, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
 class PageAllocator:
     """The library's host page allocator (pkv_alloc_*), one object per pool."""
 
@@ -201,6 +282,15 @@ class PageAllocator:
 
     def fork(self, parent: int, child: int):
         _check("pkv_alloc_fork", _lib.pkv_alloc_fork(self._h, parent, child))
+
+    def compact(self, seq_ids, new_lens):
+        """Shorten sequences as paged_kv_evict leaves them (see pkv_alloc_compact)."""
+        if len(seq_ids) != len(new_lens):
+            raise ValueError("one new length for each sequence")
+        n = len(seq_ids)
+        ids = (ctypes.c_int * max(n, 1))(*seq_ids)
+        lens = (ctypes.c_int * max(n, 1))(*new_lens)
+        _check("pkv_alloc_compact", _lib.pkv_alloc_compact(self._h, ids, n, lens))
 
     def free_seq(self, seq_id: int):
         _check("pkv_alloc_free_seq", _lib.pkv_alloc_free_seq(self._h, seq_id))

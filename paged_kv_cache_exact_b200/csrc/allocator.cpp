@@ -106,6 +106,46 @@ int pkv_alloc_fork(pkv_allocator* a, int parent_id, int child_id) {
   return PKV_OK;
 }
 
+int pkv_alloc_compact(pkv_allocator* a, const int* seq_ids, int n, const int* new_lens) {
+  if (!a || n < 0 || (n > 0 && (!seq_ids || !new_lens))) return PKV_ERR_INVALID_ARG;
+  try {
+    std::set<int> seen;
+    // What is shared is what was shared before the call: a page that two of
+    // these sequences hold is a source of both, so neither may write it.
+    std::vector<std::vector<int32_t>> next(n);
+    size_t fresh = 0;
+    for (int i = 0; i < n; ++i) {
+      auto it = a->seqs.find(seq_ids[i]);
+      if (it == a->seqs.end() || !seen.insert(seq_ids[i]).second) return PKV_ERR_INVALID_ARG;
+      const pkv_allocator::Seq& s = it->second;
+      if (new_lens[i] < 0 || new_lens[i] > s.len) return PKV_ERR_INVALID_ARG;
+      const size_t need = ((size_t)new_lens[i] + a->page_size - 1) / a->page_size;
+      next[i].assign(s.pages.begin(), s.pages.begin() + need);
+      for (int32_t& p : next[i])
+        if (a->ref[p] > 1) {
+          p = -1;
+          ++fresh;
+        }
+    }
+    if (fresh > a->free_pages.size()) return PKV_ERR_OUT_OF_PAGES;             // nothing changed
+    // Every fresh page is taken before any page is given up: none of them is a
+    // page that the call's sequences still have to be read from.
+    for (auto& pages : next)
+      for (int32_t& p : pages)
+        if (p < 0) p = a->take();
+    for (int i = 0; i < n; ++i) {
+      pkv_allocator::Seq& s = a->seqs.at(seq_ids[i]);
+      s.pages.swap(next[i]);                           // next[i]: the pages before
+      s.len = new_lens[i];
+      for (size_t k = 0; k < next[i].size(); ++k)
+        if (k >= s.pages.size() || s.pages[k] != next[i][k]) a->release(next[i][k]);
+    }
+  } catch (...) {                                      // no host memory
+    return PKV_ERR_OUT_OF_PAGES;
+  }
+  return PKV_OK;
+}
+
 int pkv_alloc_free_seq(pkv_allocator* a, int seq_id) {
   if (!a) return PKV_ERR_INVALID_ARG;
   auto it = a->seqs.find(seq_id);

@@ -1,0 +1,612 @@
+// Single-token attention over a cache held in 8 bits, and single-token
+// attention (over an 8-bit or a bf16 cache) that also adds every key's softmax
+// weight to an accumulator.
+//
+// What bounds it is reading the cache: 256 bytes (8-bit) or 512 bytes (bf16)
+// per token and kv head, plus 8 bytes of scales per block.  So every K/V row
+// is read once for all query heads of its kv head, straight from HBM into the
+// registers that feed the tensor cores: there is no shared-memory staging, and
+// a warp always has one chunk of 16 tokens in flight while it works on another.
+//
+// Products.  With up to 8 query heads per kv head (16 in two tiles) scores and
+// outputs are small matrix products, written transposed so that the long axis
+// is M: S^T = K Q^T (M = 16 tokens, N = 8 heads, 8 steps over the head dim) and
+// O^T = V^T P^T (M = 16 head dims, 8 tiles, N = 8 heads, one step of 16 tokens),
+// both mma.sync m16n8k16; tcgen05's smallest tile (M = 64 in TMEM) would be
+// three quarters padding, and the tensor pipe is far from the bound here.
+// The index that a product sums over may be permuted freely and so may the rows
+// of O^T, which is what lets each lane take 16 consecutive bytes of a row:
+//   K: lane (g, t) = (lane / 4, lane % 4) reads rows g and g + 8;
+//   V: lane (g, t) reads rows 2t, 2t+1, 2t+8, 2t+9 at bytes 16 g, and pairs of
+//      rows are interleaved in registers (prmt), which transposes V.
+// S^T comes out with a token per row and lane group, P^T goes in with a head
+// per column: one movmatrix transposes each 8 x 8 block.
+//
+// Numbers.  Codes of both formats are exact in f16, so products run on f16
+// codes: q is scaled by a power of two per head so that its largest element
+// lies in [2^14, 2^15) (f16 keeps 11 bits, bf16 has 8: exact but for elements
+// below 2^-24 of the largest, whose error is under 2^-39 of it).  P is rounded to f16, lifted by 2^7 against
+// the reference maximum so that weights down to 2^-21 of the largest keep all
+// 11 bits and those below 2^-32 of it vanish.  A bf16 cache runs on bf16
+// products and P in bf16, as in the other decode kernels.  Scales are applied
+// in float32: ks to the score, vs to each chunk's P V product (a chunk of 16
+// tokens lies in one block).  Sums and maxima are float32; the reference
+// maximum moves only when a score passes it by 2^8 (O and l share it: exact).
+//
+// Weights need the row's final maximum and sum, so the scores (float32, base-2
+// units) go to the workspace and a second kernel turns them into weights once
+// the splits are merged: each (sequence, kv head, token) is owned by one
+// thread, so there are no atomics and the sums have one order.
+#include "cache_attn.cuh"
+#include "q8.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int D = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxSplitPages = 256;               // table entries staged per CTA (16-token pages)
+constexpr int kMaxSplitTokens = 4096;
+constexpr int kMaxSplits = 1024;
+
+// d[16x8] += a[16x16] * b[16x8], f32 accumulation
+template <bool kF16>
+PKV_DEVINLINE void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                            uint32_t b0, uint32_t b1) {
+  if (kF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+PKV_DEVINLINE uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+PKV_DEVINLINE uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Codes 0,1 (lo) and 2,3 (hi) of a word as f16 pairs.
+template <int kCache>
+PKV_DEVINLINE void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kCache == PKV_I8) {
+    // code + 128 in the mantissa of 1024 + u, then minus 1152: both exact
+    const uint32_t u = w ^ 0x80808080u;
+    lo = __byte_perm(u, 0x64646464u, 0x4140);
+    hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+  }
+}
+
+template <int kCache>
+struct Layout {
+  static constexpr bool kBf16 = kCache == PKV_BF16;
+  static constexpr int kRowBytes = D * (kBf16 ? 2 : 1);
+  static constexpr int kVec = kBf16 ? 8 : 4;      // 16-byte loads per lane, chunk and matrix
+  static constexpr int kDepth = kBf16 ? 1 : 2;    // chunks in registers per warp
+  static constexpr float kLift = kBf16 ? 0.f : 7.f;
+};
+
+// Registers of one chunk of 16 tokens.
+template <int kCache>
+struct Chunk {
+  uint4 k[Layout<kCache>::kVec], v[Layout<kCache>::kVec];
+  float ks, vs;
+  int tok;           // first token
+  bool page_ok;
+};
+
+template <int kCache, int NT, bool kWeights>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+cache_decode_kernel(const CacheAttnParams p) {
+  using Lay = Layout<kCache>;
+  constexpr bool kBf16 = Lay::kBf16;
+  constexpr int kHeads = 8 * NT;
+  __shared__ int s_pages[kMaxSplitPages];
+  __shared__ __align__(16) float s_o[kWarps][kHeads][D];
+  __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const int split = blockIdx.x, s = blockIdx.z;
+  const int group = p.H / p.H_kv;
+  const int n_hg = (group + kHeads - 1) / kHeads;
+  const int kvh = blockIdx.y / n_hg;
+  const int hg0 = (blockIdx.y % n_hg) * kHeads;             // first head within the group
+  const int h0 = kvh * group + hg0;
+  const int nh = min(kHeads, group - hg0);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+
+  int L = p.seq_lens[s];
+  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  if (L < 1 || L > cap) {
+    if (split == 0 && blockIdx.y == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
+    L = max(0, min(L, cap));
+  }
+  if (L <= 0) {
+    if (split == 0)
+      for (int i = tid; i < nh * D; i += kThreads)
+        p.out[((size_t)s * p.H + h0) * D + i] = __float2bfloat16_rn(0.f);
+    return;
+  }
+  const int t_begin = split * p.split_tokens;
+  if (t_begin >= L) return;
+  const int t_end = min(L, t_begin + p.split_tokens);
+  const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
+
+  const int lp0 = t_begin >> p.page_shift;
+  const int lp1 = (t_end - 1) >> p.page_shift;
+  for (int i = tid; i <= lp1 - lp0; i += kThreads) {
+    int phys = p.block_table[(size_t)s * p.max_pages + lp0 + i];
+    if (phys < 0 || phys >= p.num_pages) {
+      flag_error(p.err, PKV_DEVERR_BAD_PAGE);
+      phys = -1;
+    }
+    s_pages[i] = phys;
+  }
+
+  // Q^T as the B operand: column n = g is head g, and each lane holds the head
+  // dims that its K loads bring (see the loads below).
+  uint32_t qb[NT][D / 16][2];
+  float hm[NT][2];                                           // score multiplier of heads 2 t4, 2 t4 + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const bool live = 8 * nt + g < nh;
+    const char* qrow = reinterpret_cast<const char*>(p.q + ((size_t)s * p.H + h0 + (live ? 8 * nt + g : 0)) * D);
+    if (kBf16) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {                          // d = 32 c + 8 t4 + 0 .. 7
+        const uint4 x = *reinterpret_cast<const uint4*>(qrow + 64 * c + 16 * t4);
+        qb[nt][2 * c][0] = live ? x.x : 0u;
+        qb[nt][2 * c][1] = live ? x.y : 0u;
+        qb[nt][2 * c + 1][0] = live ? x.z : 0u;
+        qb[nt][2 * c + 1][1] = live ? x.w : 0u;
+      }
+      hm[nt][0] = hm[nt][1] = p.scale_log2;
+    } else {
+      uint4 x[4];
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                          // d = 64 c + 16 t4 + 0 .. 15
+        x[2 * c] = *reinterpret_cast<const uint4*>(qrow + 128 * c + 32 * t4);
+        x[2 * c + 1] = *reinterpret_cast<const uint4*>(qrow + 128 * c + 32 * t4 + 16);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the head's largest element is in [2^e, 2^(e+1)): multiply by 2^(14 - e)
+      const int e = max((int)(top >> 7) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + max(14 - e, -126)) << 23);
+      const float down = __uint_as_float((uint32_t)(127 + min(e - 14, 126)) << 23);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {                        // step 4 c + w: d = 64 c + 16 t4 + 4 w + 0 .. 3
+          const uint4 y = x[2 * c + (w >> 1)];
+          const uint32_t lo = (w & 1) ? y.z : y.x, hi = (w & 1) ? y.w : y.y;
+          qb[nt][4 * c + w][0] = live ? pack_f16x2(bf16lo(lo) * up, bf16hi(lo) * up) : 0u;
+          qb[nt][4 * c + w][1] = live ? pack_f16x2(bf16lo(hi) * up, bf16hi(hi) * up) : 0u;
+        }
+      hm[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * t4);
+      hm[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
+    }
+  }
+  __syncthreads();                                           // s_pages ready
+
+  const size_t stride = (size_t)p.H_kv * Lay::kRowBytes;     // bytes between tokens of a page
+  const char* kbase = static_cast<const char*>(p.k_pages) + (size_t)kvh * Lay::kRowBytes;
+  const char* vbase = static_cast<const char*>(p.v_pages) + (size_t)kvh * Lay::kRowBytes;
+  const int pmask = p.page_size - 1;
+  const int n_chunks = (t_end - t_begin + 15) >> 4;
+
+  auto chunk_row = [&](int c, bool& ok) -> size_t {          // first physical row of chunk c
+    const int tok = t_begin + 16 * c;
+    const int phys = c < n_chunks ? s_pages[(tok >> p.page_shift) - lp0] : -1;
+    ok = phys >= 0;
+    return ((size_t)(ok ? phys : 0) << p.page_shift) + (tok & pmask);
+  };
+  auto load_k = [&](Chunk<kCache>& x, int c) {
+    const size_t row = chunk_row(c, x.page_ok);
+    x.tok = t_begin + 16 * c;
+    if (x.page_ok) {
+      const char* r0 = kbase + (row + g) * stride + 16 * t4;
+      const char* r1 = r0 + 8 * stride;
+#pragma unroll
+      for (int i = 0; i < Lay::kVec / 2; ++i) {
+        x.k[i] = ldg_nc_v4(r0 + 64 * i);
+        x.k[Lay::kVec / 2 + i] = ldg_nc_v4(r1 + 64 * i);
+      }
+      if (!kBf16) x.ks = __ldg(p.k_scales + (row >> p.block_shift) * p.H_kv + kvh);
+    }
+  };
+  auto load_v = [&](Chunk<kCache>& x, int c) {
+    bool ok;
+    const size_t row = chunk_row(c, ok);
+    const int tok = t_begin + 16 * c;
+    // rows past the sequence hold anything, NaN too: they are taken as zero
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * t4 + (i & 1) + 8 * (i >> 1);
+      const bool in = ok && tok + r < t_end;
+      const char* at = vbase + (row + r) * stride + 16 * g;
+      x.v[i] = in ? ldg_nc_v4(at) : make_uint4(0u, 0u, 0u, 0u);
+      if (kBf16) x.v[4 + i] = in ? ldg_nc_v4(at + 128) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (!kBf16 && ok) x.vs = __ldg(p.v_scales + (row >> p.block_shift) * p.H_kv + kvh);
+  };
+
+  float o[NT][8][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  Chunk<kCache> buf[Lay::kDepth];
+#pragma unroll
+  for (int b = 0; b < Lay::kDepth; ++b) {
+    load_k(buf[b], warp + b * kWarps);
+    load_v(buf[b], warp + b * kWarps);
+  }
+  for (int c0 = warp; c0 < n_chunks; c0 += kWarps * Lay::kDepth) {
+#pragma unroll
+    for (int b = 0; b < Lay::kDepth; ++b) {
+      const int c = c0 + b * kWarps;
+      if (c >= n_chunks) break;
+      Chunk<kCache>& x = buf[b];
+      const int tok = x.tok;
+      const bool page_ok = x.page_ok;
+      // S^T = K Q^T
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      if (page_ok) {
+        const uint32_t* kw = reinterpret_cast<const uint32_t*>(x.k);
+#pragma unroll
+        for (int st = 0; st < 8; ++st) {
+          uint32_t a0, a1, a2, a3;
+          if (kBf16) {
+            a0 = kw[2 * st], a2 = kw[2 * st + 1];
+            a1 = kw[16 + 2 * st], a3 = kw[16 + 2 * st + 1];
+          } else {
+            codes_to_f16<kCache>(kw[st], a0, a2);
+            codes_to_f16<kCache>(kw[8 + st], a1, a3);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816<!kBf16>(sc[nt], a0, a1, a2, a3, qb[nt][st][0], qb[nt][st][1]);
+        }
+      }
+      const float ks = kBf16 ? 1.f : x.ks;
+      load_k(x, c + kWarps * Lay::kDepth);
+
+      // scores of tokens g, g + 8 and heads 2 t4, 2 t4 + 1 in base-2 units
+      const bool in0 = page_ok && tok + g < t_end, in1 = page_ok && tok + g + 8 < t_end;
+      bool passed = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float f0 = hm[nt][0] * ks, f1 = hm[nt][1] * ks;
+        sc[nt][0] = in0 ? sc[nt][0] * f0 : -INFINITY;
+        sc[nt][1] = in0 ? sc[nt][1] * f1 : -INFINITY;
+        sc[nt][2] = in1 ? sc[nt][2] * f0 : -INFINITY;
+        sc[nt][3] = in1 ? sc[nt][3] * f1 : -INFINITY;
+        passed = passed || fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + (Lay::kLift + 8.f) ||
+                 fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + (Lay::kLift + 8.f);
+      }
+      if (kWeights) {
+        // [S, H_kv, tokens, group]; tokens past the sequence are not written
+        float* lg = p.logits + (((size_t)s * p.H_kv + kvh) * p.logit_tokens + tok + g) * group + hg0 + 2 * t4;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool in = tok + g + 8 * e < t_end;
+            float* at = lg + (size_t)(8 * e) * group + 8 * nt;
+            if ((group & 1) == 0) {
+              if (in && 8 * nt + 2 * t4 < nh)
+                *reinterpret_cast<float2*>(at) = make_float2(sc[nt][2 * e], sc[nt][2 * e + 1]);
+            } else {
+              if (in && 8 * nt + 2 * t4 < nh) at[0] = sc[nt][2 * e];
+              if (in && 8 * nt + 2 * t4 + 1 < nh) at[1] = sc[nt][2 * e + 1];
+            }
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float mx = fmaxf(sc[nt][j], sc[nt][2 + j]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (mx > m[nt][j] + (Lay::kLift + 8.f)) {
+              const float mn = mx - Lay::kLift;
+              const float a = ex2(m[nt][j] - mn);            // from -inf: 0
+              m[nt][j] = mn;
+              l[nt][j] *= a;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                o[nt][i][j] *= a;
+                o[nt][i][2 + j] *= a;
+              }
+            }
+          }
+      }
+      // P^T as the B operand: column n = head, rows = the chunk's tokens
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float p0 = ex2(sc[nt][0] - s0), p1 = ex2(sc[nt][1] - s1);
+        const float p2 = ex2(sc[nt][2] - s0), p3 = ex2(sc[nt][3] - s1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        pb[nt][0] = transpose8x8(kBf16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1));
+        pb[nt][1] = transpose8x8(kBf16 ? pack_bf16x2(p2, p3) : pack_f16x2(p2, p3));
+      }
+      // O^T += vs V^T P^T
+      const float vs = kBf16 || !page_ok ? 1.f : x.vs;
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(x.v);
+      if (page_ok) {
+        if (kBf16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {                      // word i of rows 2t, 2t+1, 2t+8, 2t+9
+            const int b0 = (i >> 2) * 16 + (i & 3);
+            const uint32_t r0 = vw[b0], r1 = vw[b0 + 4], r2 = vw[b0 + 8], r3 = vw[b0 + 12];
+            const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
+            const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816<false>(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            // bytes 4w .. 4w+3 of rows (2t, 2t+1) and (2t+8, 2t+9), interleaved by row
+            uint32_t a[4], bq[4];
+            codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x5140), a[0], a[1]);
+            codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x7362), a[2], a[3]);
+            codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x5140), bq[0], bq[1]);
+            codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x7362), bq[2], bq[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {                  // tile 2w + e: head dims 16 g + 4w + 2e, + 1
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<true>(acc, a[2 * e], a[2 * e + 1], bq[2 * e], bq[2 * e + 1], pb[nt][0], pb[nt][1]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[nt][2 * w + e][q] = fmaf(vs, acc[q], o[nt][2 * w + e][q]);
+              }
+          }
+        }
+      }
+      load_v(x, c + kWarps * Lay::kDepth);
+    }
+  }
+
+  // merge the warps
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float v = l[nt][j];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      const int head = 8 * nt + 2 * t4 + j;
+      if (g == 0) {
+        s_m[warp][head] = m[nt][j];
+        s_l[warp][head] = v;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = 2 * i;                                 // of this lane's 16 head dims
+        const int d = kBf16 ? (e >> 3) * 64 + 8 * g + (e & 7) : 16 * g + e;
+        *reinterpret_cast<float2*>(&s_o[warp][head][d]) = make_float2(o[nt][i][j], o[nt][i][2 + j]);
+      }
+    }
+  __syncthreads();
+  for (int i = tid; i < nh * D; i += kThreads) {
+    const int r = i / D, col = i % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+    float acc = 0.f, lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float wt = s_m[w][r] == -INFINITY && M == -INFINITY ? 1.f : ex2(s_m[w][r] - M);
+      acc = fmaf(wt, s_o[w][r][col], acc);
+      lsum = fmaf(wt, s_l[w][r], lsum);
+    }
+    const size_t sh = (size_t)s * p.H + h0 + r;
+    if (nsplit == 1)
+      p.out[sh * D + col] = __float2bfloat16_rn(lsum == 0.f ? 0.f : acc / lsum);
+    else
+      p.ws_o[(sh * p.max_splits + split) * D + col] = acc;
+    if (col == 0 && (kWeights || nsplit > 1)) p.ws_ml[sh * p.max_splits + split] = make_float2(M, lsum);
+  }
+}
+
+// (max, sum) of all splits of one (sequence, head), by a whole warp.
+PKV_DEVINLINE void merge_ml(const float2* ml, int nsplit, int lane, float& M, float& lsum) {
+  M = -INFINITY;
+  for (int j = lane; j < nsplit; j += 32) M = fmaxf(M, ml[j].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  lsum = 0.f;
+  for (int j = lane; j < nsplit; j += 32) {
+    const float2 v = ml[j];
+    lsum = fmaf(v.x == -INFINITY && M == -INFINITY ? 1.f : ex2(v.x - M), v.y, lsum);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+}
+
+// Splits -> output: one warp per (sequence, head), lane i owns head dims 4i .. 4i+3.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const CacheAttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long sh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (sh >= (long long)p.num_seqs * p.H) return;
+  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int L = max(0, min(p.seq_lens[sh / p.H], cap));
+  const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
+  if (nsplit <= 1) return;
+  const float2* ml = p.ws_ml + sh * p.max_splits;
+  float M, lsum;
+  merge_ml(ml, nsplit, lane, M, lsum);
+  const float4* po = reinterpret_cast<const float4*>(p.ws_o + sh * p.max_splits * D) + lane;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = 0; j < nsplit; ++j) {
+    const float mj = ml[j].x;
+    const float w = mj == -INFINITY && M == -INFINITY ? 1.f : ex2(mj - M);
+    const float4 x = po[(size_t)j * (D / 4)];
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  const bool none = lsum == 0.f;
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(p.out + sh * D) + 2 * lane;
+  out[0] = __floats2bfloat162_rn(none ? 0.f : acc.x / lsum, none ? 0.f : acc.y / lsum);
+  out[1] = __floats2bfloat162_rn(none ? 0.f : acc.z / lsum, none ? 0.f : acc.w / lsum);
+}
+
+// Scores -> weights: grid = (token ranges, kv head, sequence).  Each thread owns
+// tokens; a token's weight is the sum over the group's heads of 2^(x - lse).
+constexpr int kWeightThreads = 256;
+constexpr int kWeightTokens = 1024;               // tokens a CTA
+constexpr int kMaxGroup = 256;                    // query heads per kv head
+__global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const CacheAttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float s_lse[kMaxGroup];
+  const int kvh = blockIdx.y, s = blockIdx.z;
+  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int L = max(0, min(p.seq_lens[s], cap));
+  const int t0 = blockIdx.x * kWeightTokens;
+  if (t0 >= L) return;
+  const int group = p.H / p.H_kv;
+  const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
+  for (int h = threadIdx.x >> 5; h < group; h += kWeightThreads / 32) {
+    float M, lsum;
+    merge_ml(p.ws_ml + ((size_t)s * p.H + kvh * group + h) * p.max_splits, nsplit, threadIdx.x & 31, M, lsum);
+    // no visible key: every score is -inf, and 2^(-inf - 0) = 0
+    if ((threadIdx.x & 31) == 0) s_lse[h] = lsum == 0.f ? 0.f : M + log2f(lsum);
+  }
+  __syncthreads();
+  const size_t sk = (size_t)s * p.H_kv + kvh;
+  const float* lg = p.logits + sk * p.logit_tokens * group;
+  float* w = p.weights + sk * p.weights_stride;
+  for (int t = t0 + threadIdx.x; t < min(L, t0 + kWeightTokens); t += kWeightThreads) {
+    const float* x = lg + (size_t)t * group;
+    float sum = 0.f;
+    if ((group & 3) == 0) {
+      for (int h = 0; h < group; h += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(x + h);
+        sum += (ex2(v.x - s_lse[h]) + ex2(v.y - s_lse[h + 1])) + (ex2(v.z - s_lse[h + 2]) + ex2(v.w - s_lse[h + 3]));
+      }
+    } else {
+      for (int h = 0; h < group; ++h) sum += ex2(x[h] - s_lse[h]);
+    }
+    w[t] += sum;
+  }
+}
+
+template <int kCache, bool kWeights>
+cudaError_t launch_decode(const CacheAttnParams& p, cudaStream_t stream) {
+  const int group = p.H / p.H_kv;
+  const int heads = group > 8 ? 16 : 8;
+  const dim3 grid(p.max_splits, p.H_kv * ((group + heads - 1) / heads), p.num_seqs);
+  if (group > 8)
+    cache_decode_kernel<kCache, 2, kWeights><<<grid, kThreads, 0, stream>>>(p);
+  else
+    cache_decode_kernel<kCache, 1, kWeights><<<grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// The kernel after the split kernel, as its programmatic dependent: it may be
+// scheduled while the split kernel drains and waits for its results itself.
+template <typename Kernel>
+cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, const CacheAttnParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_size, int* split_tokens,
+                       int* max_splits) {
+  const int group = H / H_kv;
+  const int heads = group > 8 ? 16 : 8;
+  const long long pairs = (long long)num_seqs * H_kv * ((group + heads - 1) / heads);
+  int st = 64 < page_size ? page_size : 64;
+  // double while at least 8 CTAs per SM remain
+  while (st < kMaxSplitTokens && pairs * ((max_seq_len + 2LL * st - 1) / (2LL * st)) >= 148LL * 8) st *= 2;
+  while (((long long)max_seq_len + st - 1) / st > kMaxSplits && st < kMaxSplitTokens) st *= 2;
+  *split_tokens = st;
+  *max_splits = (int)(((long long)max_seq_len + st - 1) / st);
+}
+
+cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
+  const bool w = p.weights != nullptr;
+  cudaError_t e;
+  if (p.cache_dtype == PKV_I8)
+    e = w ? launch_decode<PKV_I8, true>(p, stream) : launch_decode<PKV_I8, false>(p, stream);
+  else if (p.cache_dtype == PKV_E4M3)
+    e = w ? launch_decode<PKV_E4M3, true>(p, stream) : launch_decode<PKV_E4M3, false>(p, stream);
+  else
+    e = w ? launch_decode<PKV_BF16, true>(p, stream) : cudaErrorNotSupported;
+  if (e != cudaSuccess) return e;
+  if (p.max_splits > 1) {
+    const long long rows = (long long)p.num_seqs * p.H;
+    e = launch_after(cache_merge_kernel, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+                     kMergeWarps * 32, p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (w)
+    e = launch_after(cache_weights_kernel,
+                     dim3((p.max_seq_len + kWeightTokens - 1) / kWeightTokens, p.H_kv, p.num_seqs),
+                     kWeightThreads, p, stream);
+  return e;
+}
+
+}  // namespace pkv

@@ -1,0 +1,205 @@
+// The write side of the 8-bit paged cache: new tokens' K/V rows quantised into
+// their pages, and whole pages copied with their scales (copy-on-write).
+//
+// Each block of `block_tokens` tokens of a page has one scale per kv head.  A
+// call that writes rows of a block takes the largest magnitude `amax` of those
+// rows and sets
+//
+//     s_new = max(s_old, amax / qmax, 2^-126)      (s_old = 0 where the call
+//                                                   writes the block's token 0)
+//     code(new rows)  = RNE(x / s_new)
+//     code(old rows)  = RNE(code * s_old / s_new)  where s_new > s_old
+//
+// so a block never clips.  Quotients are rounded exactly (q8.cuh): the result
+// does not depend on how a prompt was cut into calls other than through the
+// definition above.
+//
+// One CTA per (block, call): the block's rows of every head, K and V.  A warp
+// owns one (head, K or V) at a time: lane i holds elements 4i .. 4i+3 of a
+// row, so a row of new values is one 256-byte load, its codes one 128-byte
+// store, and the maximum one shuffle reduction per block.  The bound is HBM:
+// 2 bytes read and 1 written per element.
+#include "cache_attn.cuh"
+#include "q8.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int D = 128;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// Four consecutive elements of a new row as stored (bf16 or f32).
+template <typename T> struct Row4;
+template <> struct Row4<__nv_bfloat16> {
+  uint2 w;
+  PKV_DEVINLINE void load(const void* base, size_t row, int lane) {
+    w = *reinterpret_cast<const uint2*>(static_cast<const char*>(base) + (row * 32 + lane) * 8);
+  }
+  // magnitudes compare as integers; NaN and infinity are the largest
+  PKV_DEVINLINE uint32_t amax() const {
+    const uint32_t m = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
+  }
+  PKV_DEVINLINE float at(int i) const {
+    const uint32_t v = i < 2 ? w.x : w.y;
+    return (i & 1) ? bf16hi(v) : bf16lo(v);
+  }
+};
+template <> struct Row4<float> {
+  uint4 w;
+  PKV_DEVINLINE void load(const void* base, size_t row, int lane) {
+    w = *reinterpret_cast<const uint4*>(static_cast<const char*>(base) + (row * 32 + lane) * 16);
+  }
+  PKV_DEVINLINE uint32_t amax() const {
+    return max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
+  }
+  PKV_DEVINLINE float at(int i) const {
+    return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+  }
+};
+
+// Item i of the grid -> (sequence, block of the sequence).  Sequence s owns the
+// items from cu_new[s] / block + 2 s on, which leaves room for every block its
+// rows can touch: n rows touch at most floor(n / block) + 2 blocks.
+template <int kCache, typename T>
+__global__ void __launch_bounds__(kThreads) append_q8_kernel(const AppendQ8Params p) {
+  __shared__ int s_row0, s_rows, s_off, s_dst;
+  if (threadIdx.x == 0) {
+    const int item = blockIdx.x;
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((p.cu_new[mid] >> p.block_shift) + 2 * mid <= item) lo = mid; else hi = mid - 1;
+    }
+    const int s = lo;
+    const int c0 = p.cu_new[s], n = p.cu_new[s + 1] - c0;
+    const int start = p.start_pos[s];
+    const int k = item - ((c0 >> p.block_shift) + 2 * s);        // k-th block of this sequence's rows
+    const int bt = 1 << p.block_shift;
+    int rows = 0, row0 = 0, off = 0, dst = -1;
+    if (n > 0 && c0 >= 0 && c0 + n <= p.num_new) {
+      if (start < 0) {
+        if (k == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
+      } else {
+        const long long pos = max((long long)start, (((long long)start >> p.block_shift) + k) << p.block_shift);
+        const long long end = min((long long)start + n, ((pos >> p.block_shift) + 1) << p.block_shift);
+        if (pos < end) {
+          rows = (int)(end - pos);
+          row0 = c0 + (int)(pos - start);
+          off = (int)(pos & (bt - 1));
+          const long long lp = pos >> p.page_shift;
+          if (lp >= p.max_pages) {
+            flag_error(p.err, PKV_DEVERR_BAD_LEN);
+          } else {
+            const int phys = p.block_table[(size_t)s * p.max_pages + lp];
+            if (phys < 0 || phys >= p.num_pages)
+              flag_error(p.err, PKV_DEVERR_BAD_PAGE);
+            else                                                   // block index in the pool
+              dst = (phys << (p.page_shift - p.block_shift)) +
+                    (int)((pos & (p.page_size - 1)) >> p.block_shift);
+          }
+        }
+      }
+    }
+    s_rows = rows, s_row0 = row0, s_off = off, s_dst = dst;
+  }
+  __syncthreads();
+  const int rows = s_rows, row0 = s_row0, off = s_off, dst = s_dst;
+  if (rows == 0 || dst < 0) return;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int pair = warp; pair < 2 * p.H_kv; pair += kWarps) {
+    const int h = pair >> 1;
+    const void* src = (pair & 1) ? p.v_new : p.k_new;
+    uint8_t* pages = static_cast<uint8_t*>((pair & 1) ? p.v_pages : p.k_pages);
+    float* scale = ((pair & 1) ? p.v_scales : p.k_scales) + (size_t)dst * p.H_kv + h;
+    const size_t src_row = (size_t)row0 * p.H_kv + h;
+    uint32_t* code = reinterpret_cast<uint32_t*>(pages + (((size_t)dst << p.block_shift) * p.H_kv + h) * D) + lane;
+    const size_t code_stride = (size_t)p.H_kv * D / 4;              // words between tokens
+
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r) {
+      Row4<T> x;
+      x.load(src, src_row + (size_t)r * p.H_kv, lane);
+      m = max(m, x.amax());
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    const float old = off > 0 ? *scale : 0.f;
+    const bool broken = m >= 0x7f800000u || isnan(old);             // NaN or infinity: the block reads NaN
+    const float s = broken ? __uint_as_float(0x7fffffffu)
+                           : fmaxf(fmaxf(old, __fdiv_rn(__uint_as_float(m), code_max<kCache>())), kMinScale);
+    __syncwarp();                                                   // every lane has read the old scale
+    if (lane == 0) *scale = s;
+    if (off > 0 && s > old) {
+      const float ratio = __fdiv_rn(old, s);
+      for (int r = 0; r < off; ++r)
+        code[r * code_stride] = requantize4<kCache>(code[r * code_stride], ratio, old, s);
+    }
+    const float inv = __fdiv_rn(1.f, s);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      Row4<T> x;
+      x.load(src, src_row + (size_t)r * p.H_kv, lane);
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = x.at(i);
+        w |= code_of<kCache>(v * inv, [&] {
+               return code_exact<kCache>(static_cast<double>(v), static_cast<double>(s));
+             }) << (8 * i);
+      }
+      code[(size_t)(off + r) * code_stride] = broken ? 0u : w;
+    }
+  }
+}
+
+// grid = (pairs, chunks of a page): codes in 16-byte vectors, then the scales.
+__global__ void __launch_bounds__(kThreads) copy_pages_q8_kernel(const CopyPagesQ8Params p) {
+  const int src = p.src[blockIdx.x], dst = p.dst[blockIdx.x];
+  if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
+    if (blockIdx.y == 0 && threadIdx.x == 0) flag_error(p.err, PKV_DEVERR_BAD_PAGE);
+    return;
+  }
+  const size_t vec = p.page_bytes / 16;
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k_pages + (size_t)src * p.page_bytes);
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v_pages + (size_t)src * p.page_bytes);
+  uint4* kd = reinterpret_cast<uint4*>(p.k_pages + (size_t)dst * p.page_bytes);
+  uint4* vd = reinterpret_cast<uint4*>(p.v_pages + (size_t)dst * p.page_bytes);
+  for (size_t v = (size_t)blockIdx.y * kThreads + threadIdx.x; v < vec; v += (size_t)gridDim.y * kThreads) {
+    kd[v] = ks[v];
+    vd[v] = vs[v];
+  }
+  if (blockIdx.y == 0)
+    for (int i = threadIdx.x; i < p.page_scales; i += kThreads) {
+      p.k_scales[(size_t)dst * p.page_scales + i] = p.k_scales[(size_t)src * p.page_scales + i];
+      p.v_scales[(size_t)dst * p.page_scales + i] = p.v_scales[(size_t)src * p.page_scales + i];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_q8(const AppendQ8Params& p, cudaStream_t stream) {
+  const long long items = ((long long)p.num_new >> p.block_shift) + 2LL * p.num_seqs;
+  if (items > 0x7fffffffLL) return cudaErrorNotSupported;
+  const unsigned grid = (unsigned)items;
+  if (p.cache_dtype == PKV_I8) {
+    if (p.rows_f32) append_q8_kernel<PKV_I8, float><<<grid, kThreads, 0, stream>>>(p);
+    else append_q8_kernel<PKV_I8, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (p.rows_f32) append_q8_kernel<PKV_E4M3, float><<<grid, kThreads, 0, stream>>>(p);
+    else append_q8_kernel<PKV_E4M3, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_copy_pages_q8(const CopyPagesQ8Params& p, cudaStream_t stream) {
+  const size_t vec = p.page_bytes / 16;
+  unsigned chunks = (unsigned)((vec + kThreads * 4 - 1) / (kThreads * 4));     // 16 KB per CTA and matrix
+  chunks = chunks < 1 ? 1 : (chunks > 65535 ? 65535 : chunks);
+  copy_pages_q8_kernel<<<dim3(p.n, chunks), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv
