@@ -20,8 +20,9 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["pkv_api.cu", "decode.cu", "decode_noalloc.cu", "simt_fp32.cu", "prefill_sm100.cu",
-           "kv_write.cu", "allocator.cpp", "cache_api.cu", "q8_write.cu", "decode_cache.cu", "evict.cu"]
-HEADERS = ["common.cuh", "sm100_ptx.cuh", "cache_attn.cuh", "q8.cuh"]
+           "kv_write.cu", "allocator.cpp", "cache_api.cu", "q8_write.cu", "decode_cache.cu",
+           "weights_sm100.cu", "evict.cu"]
+HEADERS = ["common.cuh", "sm100_ptx.cuh", "cache_attn.cuh", "q8.cuh", "cp_async.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

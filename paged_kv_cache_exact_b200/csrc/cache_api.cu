@@ -27,6 +27,9 @@ struct Workspace {
   size_t total() const { return up256(o) + up256(ml) + up256(logits) + up256(lse); }
 };
 
+// Rows of the log2-sums a (sequence, head) has: whole tiles of the weights kernel.
+size_t lse_rows(int q_len) { return ((size_t)q_len + 127) / 128 * 128; }
+
 Workspace attn_workspace(int num_seqs, int q_len, int H, int H_kv, int max_seq_len, int page_size, bool weights) {
   Workspace w;
   if (q_len == 1) {
@@ -37,7 +40,7 @@ Workspace attn_workspace(int num_seqs, int q_len, int H, int H_kv, int max_seq_l
     if (nsplit > 1 || weights) w.ml = per * sizeof(float2);
     if (weights) w.logits = (size_t)num_seqs * H * max_seq_len * sizeof(float);
   } else if (weights) {
-    w.lse = (size_t)num_seqs * H * q_len * sizeof(float);
+    w.lse = (size_t)num_seqs * H * lse_rows(q_len) * sizeof(float);
   }
   return w;
 }
@@ -99,7 +102,20 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
     pkv::cache_decode_plan(num_seqs, H, H_kv, max_seq_len, page_size, &p.split_tokens, &p.max_splits);
     return pkv::cuda_status(pkv::launch_cache_decode(p, st));
   }
-  return PKV_ERR_UNSUPPORTED;
+  pkv::PrefillParams f{};
+  f.Q = q, f.K = k_pages, f.V = v_pages, f.O = out;
+  f.block_table = block_table, f.seq_lens = seq_lens;
+  f.err = p.err;
+  f.B = num_seqs, f.H = H, f.H_kv = H_kv, f.q_len = q_len, f.d = d;
+  f.paged = 1, f.page_size = page_size, f.page_shift = p.page_shift;
+  f.num_pages = num_pages, f.max_pages = max_pages_per_seq, f.max_seq_len = max_seq_len;
+  f.causal = causal, f.scale_log2 = p.scale_log2;
+  if (q8) f.cache_dtype = cache_dtype, f.block_shift = p.block_shift, f.k_scales = p.k_scales, f.v_scales = p.v_scales;
+  p.lse_stride = (int)lse_rows(q_len);
+  f.lse = p.lse, f.lse_stride = p.lse_stride;
+  const cudaError_t e = pkv::launch_prefill_bf16(f, st);
+  if (e != cudaSuccess || !weights) return pkv::cuda_status(e);
+  return pkv::cuda_status(pkv::launch_prompt_weights(p, st));
 }
 
 }  // namespace

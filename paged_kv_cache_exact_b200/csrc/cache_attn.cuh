@@ -46,10 +46,10 @@ struct CacheAttnParams {
   float* ws_o;                 // [S, H, max_splits, d]
   float2* ws_ml;               // [S, H, max_splits]: max in log2 units, sum
   float* logits;               // [S, H_kv, logit_tokens, H / H_kv]: scores in log2 units
-  float* lse;                  // [S, H, q_len]: log2 of each row's sum
+  float* lse;                  // [S, H, lse_stride]: log2 of each row's sum, +infinity past q_len
   unsigned int* err;
   int num_seqs, q_len, H, H_kv, page_size, page_shift, block_shift, num_pages, max_pages, max_seq_len;
-  int split_tokens, max_splits, weights_stride, logit_tokens;
+  int split_tokens, max_splits, weights_stride, logit_tokens, lse_stride;
   int cache_dtype, causal;
   float scale, scale_log2;     // scale_log2 = scale * log2(e)
 };
@@ -80,6 +80,7 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
 cudaError_t launch_append_q8(const AppendQ8Params& p, cudaStream_t stream);
 cudaError_t launch_copy_pages_q8(const CopyPagesQ8Params& p, cudaStream_t stream);
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream);
+cudaError_t launch_prompt_weights(const CacheAttnParams& p, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
 }  // namespace pkv

@@ -97,6 +97,15 @@ struct PrefillParams {
   // for it runs out; the public entry points leave it 0.
   unsigned long long wait_limit_ns;
   int stall_tile_plus1;
+  // 8-bit paged cache (K and V hold codes); zero: a bf16 cache.
+  int cache_dtype;             // PKV_I8 or PKV_E4M3
+  int block_shift;             // log2 of the tokens a scale covers
+  const float* k_scales;       // [P, ps / block, H_kv]
+  const float* v_scales;
+  // Row sums for the attention weights (null: not wanted): log2 of every row's
+  // sum, [B, H, lse_stride], lse_stride >= q_len.
+  float* lse;
+  int lse_stride;
 };
 
 struct AppendParams {

@@ -45,11 +45,24 @@
 // * A page id outside the pool is never read: its keys are left out of the
 //   softmax (as the decode kernel does) and its V rows are zeroed, and
 //   PKV_DEVERR_BAD_PAGE is recorded.
+//
+// 8-bit caches (kCache = PKV_I8 or PKV_E4M3, paged).  int8 and e4m3 codes are
+// exact in bf16, so the MMAs run on bf16 codes and the scales are applied in
+// float32: a key block's scale joins the softmax scale, a value block's scale
+// multiplies P before it is rounded to bf16.  Warps 10 and 11 take the place of
+// the TMA loads: each streams its 64 rows of a K or V tile in pieces of 16 rows
+// (a piece lies in one page and one scale block) through a ring of cp.async
+// stages, converts the codes in registers and writes the swizzled bf16 tile that
+// TMA would have written.  A lane converts exactly the bytes it copied, so a
+// piece needs no barrier, and the ring keeps kPieces pieces per warp in flight.
+// Warp 10 also does the loader's other work (Q loads, item claims); rows past
+// the sequence and rows of bad pages are written as zeros.
 #include <cuda.h>
 
 #include <mutex>
 
 #include "common.cuh"
+#include "cp_async.cuh"
 #include "sm100_ptx.cuh"
 
 namespace pkv {
@@ -112,6 +125,16 @@ constexpr int kOffTmemSlot = kOffMask + 4 * kMaskSlots;
 constexpr int kOffAbort = kOffTmemSlot + 4;
 constexpr int kSmemUsed = kOffAbort + 4;
 constexpr int kSmemBytes = kSmemUsed + 1024;       // slack for 1024-byte alignment
+
+// 8-bit caches: scales of the K/V tiles in flight, then each converter warp's
+// ring of 2 KB pieces (16 rows of 128 codes).
+constexpr int kScaleSlots = 8;
+constexpr int kPieces = 6;
+constexpr int kPieceBytes = 16 * D;
+constexpr int kOffScale = (kSmemUsed + 15) & ~15;                  // float[kScaleSlots][16]: 8 ks, 8 vs
+constexpr int kOffPiece = kOffScale + kScaleSlots * 64;
+constexpr int kSmemBytesQ8 = kOffPiece + 2 * kPieces * kPieceBytes + 1024;
+static_assert(kSmemBytesQ8 <= 227 * 1024, "shared memory");
 
 // TMEM columns.
 constexpr uint32_t kColS = 0;      // + 128 * tile
@@ -187,8 +210,32 @@ __device__ __forceinline__ Geometry item_geometry(const PrefillParams& p, int it
   return g;
 }
 
+// Four codes -> four bf16 (two words), exact.
+template <int kCache>
+PKV_DEVINLINE void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (kCache == PKV_I8) {
+    // Byte b under the high byte 0x43: bits 0..6 give 128 + (b & 127), bit 7
+    // alone gives 128 or 256; their difference is the signed code.
+    const uint32_t l = __byte_perm(w, 0x43434343u, 0x4140);
+    const uint32_t h = __byte_perm(w, 0x43434343u, 0x4342);
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(l & 0xff7fff7fu), "r"(l & 0xff80ff80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(h & 0xff7fff7fu), "r"(h & 0xff80ff80u));
+  } else {
+    // e4m3's exponent and mantissa bits under bf16's sign give the value times
+    // 2^-120 (subnormal codes too); 2^120 restores it.
+    const uint32_t l = __byte_perm(w, 0u, 0x1404);
+    const uint32_t h = __byte_perm(w, 0u, 0x3424);
+    const uint32_t a = ((l & 0x7f007f00u) >> 4) | (l & 0x80008000u);
+    const uint32_t b = ((h & 0x7f007f00u) >> 4) | (h & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x7b807b80u));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x7b807b80u));
+  }
+}
+
 // ----------------------------------------------------------------------------
-template <bool kPaged, bool kFp8QK>
+// kCache: PKV_BF16, or the code type of an 8-bit paged cache.  kLse: every row's
+// log2 of its softmax sum goes to p.lse (+infinity for a row that sees no key).
+template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
@@ -201,6 +248,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   volatile int* item_slot = reinterpret_cast<volatile int*>(smem + kOffItem);
   volatile uint32_t* mask_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffMask);
   const uint64_t limit_ns = p.wait_limit_ns ? p.wait_limit_ns : kDefaultWaitNs;
+  constexpr bool kQ8 = kCache != PKV_BF16;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -209,7 +257,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t cnt = 1;
       if (i >= kBarPHalf && i < kBarPFull + kQTiles) cnt = 128;   // one arrival per softmax thread
-      if (i >= kBarItemFree && i < kBarItemFree + 2) cnt = kItemReaders;
+      if (i >= kBarItemFree && i < kBarItemFree + 2) cnt = kItemReaders + kQ8;   // + the second converter
+      // one arrival per converting thread
+      if (kQ8 && ((i >= kBarKFull && i < kBarKFull + kStages) || (i >= kBarVFull && i < kBarVFull + kStages)))
+        cnt = 64;
       mbar_init(bar(i), cnt);
     }
     for (int s = 0; s < kMaskSlots; ++s) mask_slot[s] = mask_word(s - kMaskSlots, 0);
@@ -258,7 +309,164 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   if (warp >= 8) regs_decrease<kRegsSide>();
 
-  if (warp == 8) {
+  if (kQ8 && (warp == 10 || warp == 11)) {
+    // ------------------------------------------- loader and converters, 8-bit --
+    const int half = warp - 10;                      // rows 64 half .. 64 half + 63 of every tile
+    const bool lead = half == 0;                     // loads Q and claims items
+    const uint32_t ring = sbase + kOffPiece + half * kPieces * kPieceBytes + lane * 16;
+    float* scales = reinterpret_cast<float*>(smem + kOffScale);
+    const int ck = lane & 7, rk = lane >> 3;         // this lane's 16-byte chunk, and row + 4 u
+    const size_t stride = (size_t)p.H_kv * D;
+    int kv_it = 0, claims = 0;
+    int q_it[kQTiles] = {0, 0};
+    uint32_t q_pend = 0;                             // Q tile t: bit t loads pending, bit 2 + t their parity
+    bool pend_claim = false, claim_live = true, ok = true;
+    if (lead && lane == 0) prefetch_tmap(&tmQ);
+    int item = blockIdx.x;
+    for (int k = 0; ok && item >= 0; ++k) {
+      const Geometry g = item_geometry(p, item);
+      const int nmax = g.nmax;
+      if (lead && lane == 0 && g.bad_len && g.q0 == 0 && g.h == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
+      bool claimed = false;
+      auto claim = [&]() {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarClaim), 16);
+          clc_try_cancel(sbase + kOffClaim, bar(kBarClaim));
+        }
+        __syncwarp();
+        claimed = true;
+        pend_claim = true;
+      };
+      auto load_q = [&](int t) -> bool {
+        if (!wwait(kBarQEmpty + t, (q_it[t] & 1) ^ 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarQFull + t), kTileBytes);
+          for (int c = 0; c < 2; ++c)
+            tma_load_3d(sbase + kOffQ + t * kTileBytes + c * kHalfBytes, &tmQ, c * 64,
+                        g.q0 + t * BM, g.b * p.H + g.h, bar(kBarQFull + t));
+        }
+        __syncwarp();
+        q_pend = (q_pend & ~(5u << t)) | (1u << t) | ((uint32_t)(q_it[t] & 1) << (2 + t));
+        return true;
+      };
+      const uint8_t* kb = static_cast<const uint8_t*>(p.K) + (size_t)g.kvh * D + ck * 16;
+      const uint8_t* vb = static_cast<const uint8_t*>(p.V) + (size_t)g.kvh * D + ck * 16;
+      const int32_t* trow = p.block_table + (size_t)g.b * p.max_pages;
+      const int n_pages = (g.kv_len + p.page_size - 1) >> p.page_shift;
+      // Pieces of this warp: tile j has 4 of K, then 4 of V.
+      const int total = nmax * 8;
+      int held = -32, entry = -1;                    // lane l holds the table entry of page held + l
+      auto fetch = [&](int q) {                      // start piece q's copy (always commits a group)
+        if (q < total) {
+          const int j = q >> 3;
+          const int r0 = 64 * half + 16 * (q & 3);   // first row in the tile
+          const int tok = j * BN + r0;
+          const int page = tok >> p.page_shift;
+          if (page < held || page >= held + 32) {    // warp-uniform
+            held = page;
+            entry = page + lane < n_pages ? trow[page + lane] : -1;
+          }
+          const int phys = __shfl_sync(0xffffffffu, entry, page - held);
+          const bool live = tok < g.kv_len;
+          const bool good = live && phys >= 0 && phys < p.num_pages;
+          const size_t row = good ? (((size_t)phys << p.page_shift) + (tok & (p.page_size - 1))) : 0;
+          const uint8_t* src = (q & 4) ? vb : kb;
+          const uint32_t dst = ring + (q % kPieces) * kPieceBytes;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            cp_async16(dst + u * 512, src + (row + rk + 4 * u) * stride,
+                       good && tok + rk + 4 * u < g.kv_len);
+          if (!(q & 4) && lane < 2) {                // with K: both scales of the piece
+            float* slot = scales + ((kv_it + j) % kScaleSlots) * 16 + lane * 8 + (r0 >> 4);
+            if (good) {
+              const float* from = (lane ? p.v_scales : p.k_scales) + (row >> p.block_shift) * p.H_kv + g.kvh;
+              cp_async4(smem_u32(slot), from);
+            } else {
+              *slot = live && lane == 0 ? -1.f : 1.f;    // a negative key scale: keys of a bad page
+            }
+            if (live && !good && lane == 0) flag_error(p.err, PKV_DEVERR_BAD_PAGE);
+          }
+        }
+        cp_async_commit();
+      };
+#pragma unroll 1
+      for (int q = 0; q < kPieces; ++q) fetch(q);
+      if (lead && g.n[0] > 0) ok = load_q(0);
+      if (ok && lead && g.n[1] > 0) ok = load_q(1);
+#pragma unroll 1
+      for (int q = 0; q < total && ok; ++q) {
+        const int it = kv_it + (q >> 3);
+        const int st = it % kStages;
+        const bool is_v = q & 4;
+        if ((q & 3) == 0) {
+          if (lead && !claimed && claim_live && (q >> 3) >= nmax - kClaimLead) claim();
+          ok = wwait((is_v ? kBarVEmpty : kBarKEmpty) + st, ((it / kStages) & 1) ^ 1);
+          if (!ok) break;
+        }
+        cp_async_wait<kPieces - 1>();
+        const uint8_t* raw = smem + kOffPiece + half * kPieces * kPieceBytes + (q % kPieces) * kPieceBytes + lane * 16;
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * 512);
+        uint8_t* tile = smem + (is_v ? kOffV : kOffK) + st * kTileBytes + (ck >> 2) * kHalfBytes;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 64 * half + 16 * (q & 3) + rk + 4 * u;
+          uint4 a, b;
+          codes_to_bf16<kCache>(x[u].x, a.x, a.y);
+          codes_to_bf16<kCache>(x[u].y, a.z, a.w);
+          codes_to_bf16<kCache>(x[u].z, b.x, b.y);
+          codes_to_bf16<kCache>(x[u].w, b.z, b.w);
+          // chunks 2c, 2c + 1 of the row's 64-column block; the lanes of the second
+          // block store them the other way round, so that 8 lanes meet 8 banks' groups
+          const int c0 = 2 * (ck & 3);
+          const bool swap = ck >= 4;
+          uint8_t* at = tile + r * 128;
+          *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? b : a;
+          *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (r & 7)) << 4)) = swap ? a : b;
+        }
+        if ((q & 3) == 3) {
+          fence_proxy_async_smem();
+          mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
+        }
+        fetch(q + kPieces);
+      }
+      if (!ok) break;
+      cp_async_wait<0>();
+      int next = -1;
+      if (lead) {
+        if (!claimed && claim_live) claim();
+        if (claim_live) {
+          ok = wwait(kBarClaim, claims & 1);
+          if (!ok) break;
+          pend_claim = false;
+          ++claims;
+          next = __shfl_sync(0xffffffffu, lane == 0 ? clc_cancelled_x(sbase + kOffClaim) : 0, 0);
+          if (next < 0) claim_live = false;
+        }
+        ok = wwait(kBarItemFree + (k & 1), ((k >> 1) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          item_slot[k & 1] = next;
+          mbar_arrive(bar(kBarItem + (k & 1)));
+        }
+        __syncwarp();
+      } else {
+        next = read_item(k);
+        if (next == -2) ok = false;
+      }
+      kv_it += nmax;
+#pragma unroll
+      for (int t = 0; t < kQTiles; ++t) q_it[t] += g.n[t] > 0;
+      item = next;
+    }
+    cp_async_wait<0>();
+    if (!ok && lead && lane == 0) {
+      for (int t = 0; t < kQTiles; ++t)
+        if ((q_pend >> t) & 1) mbar_wait_bounded(bar(kBarQFull + t), (q_pend >> (2 + t)) & 1, limit_ns);
+      if (pend_claim) mbar_wait_bounded(bar(kBarClaim), claims & 1, limit_ns);
+    }
+  } else if (!kQ8 && warp == 8) {
     // ------------------------------------------------------------- loader --
     // The warp runs converged.  Contiguous tiles and pages of >= 128 tokens
     // take one TMA box per 64-column block, issued by lane 0; shorter pages
@@ -474,7 +682,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const Geometry g = item_geometry(p, item);
       const int nmax = g.nmax;
       if (nmax == 0) continue;
-      const bool last_fix = kPaged && g.kv_len - (nmax - 1) * BN < BN;
+      const bool last_fix = kPaged && !kQ8 && g.kv_len - (nmax - 1) * BN < BN;
       int s_left[kQTiles] = {g.n[0], g.n[1]};
       auto commit = [&](int b) {
         if (leader) mma_commit(bar(b));
@@ -607,7 +815,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (!ok) break;
         ++s_it;
         uint32_t bad_keys[4] = {0u, 0u, 0u, 0u};      // keys of pages outside the pool
-        if (kPaged) {
+        float ks[8], vs[8];                           // 8-bit: scales of the tile's 16-key groups
+        if (kQ8) {
+          // Written before the K tile was handed over, so visible through S.
+          const float4* slot = reinterpret_cast<const float4*>(
+              smem + kOffScale + ((kv_it + j) % kScaleSlots) * 64);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 a = slot[i], b = slot[2 + i];
+            ks[4 * i] = a.x, ks[4 * i + 1] = a.y, ks[4 * i + 2] = a.z, ks[4 * i + 3] = a.w;
+            vs[4 * i] = b.x, vs[4 * i + 1] = b.y, vs[4 * i + 2] = b.z, vs[4 * i + 3] = b.w;
+          }
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            if (ks[b] < 0.f) bad_keys[b >> 1] |= 0xFFFFu << (16 * (b & 1));
+            // A NaN value scale makes every row that sees the block NaN; said through
+            // the key scale, which masking keeps from rows that do not see it.
+            if (isnan(vs[b])) ks[b] = vs[b], vs[b] = 1.f;
+          }
+        } else if (kPaged) {
           // Keys of pages outside the pool are left out (their K rows were
           // never loaded).  The loader wrote this tile's mask before its K load.
           const int it = kv_it + j;
@@ -661,22 +887,40 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                           : first_hidden >= 32 ? 0u : (0xFFFFFFFFu << first_hidden);
             if (kPaged) hide |= bad_keys[q];
 #pragma unroll
-            for (int b = 0; b < 32; ++b)
+            for (int b = 0; b < 32; ++b) {
+              if (kQ8) s[32 * q + b] = __float_as_uint(__uint_as_float(s[32 * q + b]) * ks[2 * q + (b >> 4)]);
               if ((hide >> b) & 1u) s[32 * q + b] = __float_as_uint(-INFINITY);
+            }
+          }
+          if (kQ8) {
+#pragma unroll
+            for (int b = 0; b < 8; ++b) ks[b] = 1.f;      // applied above
           }
         }
         // row max: eight chains of 3-input max (dependency depth 8)
         float am[8];
+        if (kQ8) {                                     // a chain per 16-key group, then its scale
 #pragma unroll
-        for (int a = 0; a < 8; ++a) am[a] = __uint_as_float(s[a]);
+          for (int b = 0; b < 8; ++b) am[b] = __uint_as_float(s[16 * b]);
 #pragma unroll
-        for (int i = 8; i + 16 <= 128; i += 16) {        // elements 8 .. 119
+          for (int i = 1; i + 2 <= 16; i += 2)
 #pragma unroll
-          for (int a = 0; a < 8; ++a)
-            am[a] = max3(am[a], __uint_as_float(s[i + 2 * a]), __uint_as_float(s[i + 2 * a + 1]));
+            for (int b = 0; b < 8; ++b)
+              am[b] = max3(am[b], __uint_as_float(s[16 * b + i]), __uint_as_float(s[16 * b + i + 1]));
+#pragma unroll
+          for (int b = 0; b < 8; ++b) am[b] = fmaxf(am[b], __uint_as_float(s[16 * b + 15])) * ks[b];
+        } else {
+#pragma unroll
+          for (int a = 0; a < 8; ++a) am[a] = __uint_as_float(s[a]);
+#pragma unroll
+          for (int i = 8; i + 16 <= 128; i += 16) {      // elements 8 .. 119
+#pragma unroll
+            for (int a = 0; a < 8; ++a)
+              am[a] = max3(am[a], __uint_as_float(s[i + 2 * a]), __uint_as_float(s[i + 2 * a + 1]));
+          }
+#pragma unroll
+          for (int a = 0; a < 8; ++a) am[a] = fmaxf(am[a], __uint_as_float(s[120 + a]));   // 120 .. 127
         }
-#pragma unroll
-        for (int a = 0; a < 8; ++a) am[a] = fmaxf(am[a], __uint_as_float(s[120 + a]));   // 120 .. 127
         const float mx = max3(max3(am[0], am[1], am[2]), max3(am[3], am[4], am[5]),
                               fmaxf(am[6], am[7]));
         const uint64_t c2 = f2(c, c);
@@ -686,13 +930,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int e = 64 * ch + 2 * i;
-            const uint64_t x2 = fma2(f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nm2);
+            const float ce = kQ8 ? c * ks[e >> 4] : c;
+            const uint64_t x2 = fma2(f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                     kQ8 ? f2(ce, ce) : c2, nm2);
             float x0, x1;
             unf2(x2, x0, x1);
             const float p0 = ex2(x0);
             const float p1 = ex2(x1);
             acc[i & 3] = add2(acc[i & 3], f2(p0, p1));
-            pk[i] = pack_bf16x2(p0, p1);
+            pk[i] = kQ8 ? pack_bf16x2(p0 * vs[e >> 4], p1 * vs[e >> 4]) : pack_bf16x2(p0, p1);
           }
         };
 #pragma unroll
@@ -744,6 +990,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc_fence_after();
       }
       const bool store = row < p.q_len;
+      if (kLse && row < p.lse_stride)                // rows past q_len (tile padding): +infinity
+        p.lse[((size_t)g.b * p.H + g.h) * p.lse_stride + row] =
+            store && n > 0 && l != 0.f ? m_ref + log2f(l) : INFINITY;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) +
                            (((size_t)g.b * p.H + g.h) * p.q_len + (store ? row : 0)) * D;
       const float inv = (n > 0 && l > 0.f) ? 1.f / l : 0.f;
@@ -823,7 +1072,7 @@ bool encode_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint6
 
 // Dynamic shared memory is a per-device function attribute; host threads may
 // launch concurrently, so the once-per-device record is kept under a lock.
-template <bool kPaged, bool kFp8QK>
+template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
 cudaError_t set_smem_attr() {
   static bool done[64] = {};
   static std::mutex mu;
@@ -835,13 +1084,24 @@ cudaError_t set_smem_attr() {
   // The in-kernel register split assumes this exact launch allocation (the
   // build checks it too).
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_kernel<kPaged, kFp8QK>);
+  e = cudaFuncGetAttributes(&fa, prefill_kernel<kPaged, kFp8QK, kCache, kLse>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-  e = cudaFuncSetAttribute(prefill_kernel<kPaged, kFp8QK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmemBytes);
+  e = cudaFuncSetAttribute(prefill_kernel<kPaged, kFp8QK, kCache, kLse>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kCache != PKV_BF16 ? kSmemBytesQ8 : kSmemBytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
+}
+
+template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
+cudaError_t launch_variant(dim3 grid, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                           const PrefillParams& p, cudaStream_t stream) {
+  const cudaError_t e = set_smem_attr<kPaged, kFp8QK, kCache, kLse>();
+  if (e != cudaSuccess) return e;
+  prefill_kernel<kPaged, kFp8QK, kCache, kLse>
+      <<<grid, kThreads, kCache != PKV_BF16 ? kSmemBytesQ8 : kSmemBytes, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -852,11 +1112,15 @@ cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t stream) {
   const uint64_t row_bytes = D * 2;
   const bool f8 = p.fp8_qk != 0;
   if (f8 && p.paged) return cudaErrorNotSupported;
+  const bool q8 = p.cache_dtype == PKV_I8 || p.cache_dtype == PKV_E4M3;   // 0 or PKV_BF16: not 8-bit
+  if (q8 && !p.paged) return cudaErrorNotSupported;
   const uint64_t qk_row = f8 ? D : row_bytes;        // e4m3 Q/K rows are 128 bytes
   // Q: [B*H, q_len, d]
   if (!encode_3d(&tq, p.Q, D, p.q_len, (uint64_t)p.B * p.H, qk_row, qk_row * p.q_len, BM, 1, f8))
     return cudaErrorInvalidValue;
-  if (p.paged) {
+  if (q8) {
+    tk = tv = tq;                                    // not read: the codes are not loaded by TMA
+  } else if (p.paged) {
     // pages [P, ps, H_kv, d] viewed as [P*ps tokens, H_kv, d]; one box = one page's rows.
     const uint32_t rows = p.page_size < BN ? p.page_size : BN;
     const uint64_t tokens = (uint64_t)p.num_pages * p.page_size;
@@ -880,27 +1144,23 @@ cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t stream) {
   PrefillParams q = p;
   {
     const long long kv_len = p.paged ? p.max_seq_len : p.kv_len;
-    const long long kv_bytes = 2LL * kv_len * D * 2;              // K and V of one kv head
+    const long long kv_bytes = 2LL * kv_len * D * (q8 ? 1 : 2);   // K and V of one kv head
     const int group_q = p.H / p.H_kv;
     long long hg = (64LL << 20) / (kv_bytes > 0 ? kv_bytes : 1) * group_q;
     hg = hg < 1 ? 1 : (hg > 32 ? 32 : hg);
     q.head_group = (int)hg;
   }
-  cudaError_t e;
-  if (p.paged) {
-    e = set_smem_attr<true, false>();
-    if (e != cudaSuccess) return e;
-    prefill_kernel<true, false><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, q);
-  } else if (f8) {
-    e = set_smem_attr<false, true>();
-    if (e != cudaSuccess) return e;
-    prefill_kernel<false, true><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, q);
-  } else {
-    e = set_smem_attr<false, false>();
-    if (e != cudaSuccess) return e;
-    prefill_kernel<false, false><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, q);
-  }
-  return cudaGetLastError();
+  if (p.cache_dtype == PKV_I8)
+    return p.lse ? launch_variant<true, false, PKV_I8, true>(grid, tq, tk, tv, q, stream)
+                 : launch_variant<true, false, PKV_I8, false>(grid, tq, tk, tv, q, stream);
+  if (p.cache_dtype == PKV_E4M3)
+    return p.lse ? launch_variant<true, false, PKV_E4M3, true>(grid, tq, tk, tv, q, stream)
+                 : launch_variant<true, false, PKV_E4M3, false>(grid, tq, tk, tv, q, stream);
+  if (p.paged)
+    return p.lse ? launch_variant<true, false, PKV_BF16, true>(grid, tq, tk, tv, q, stream)
+                 : launch_variant<true, false, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
+  if (f8) return launch_variant<false, true, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
+  return launch_variant<false, false, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
 }
 
 }  // namespace pkv

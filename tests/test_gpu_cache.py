@@ -6,7 +6,9 @@ gives 2^-8 |o|; rounding each p to the type of the product gives at most 2^-8
 (bf16 cache) or 2^-11 (8-bit cache) of sum_j p_j |v_j|.  A score is a float32
 sum of 128 products, off by at most 128 * 2^-24 of sum |q||k| * scale (and a few
 2^-24 of itself for its scales); an error e of every score changes p by a factor
-within exp(2 e), and 2^-20 covers the exponential, the sums and the division.
+within exp(2 e), and 2^-20 covers the exponential, the sums and the division.  A
+weight is 2^(x - L) with x and the row's log2-sum L in float32, both at most
+1.4427 * (sum |q||k| * scale) + log2(keys): half a step of each is 2^-24 of that.
 """
 
 import math
@@ -106,7 +108,8 @@ class Cache:
         want, ww, spread, size = attend(self.q, self.k, self.v, self.ks, self.vs, self.table, lens, causal, self.scale)
         e = 128 * 2.0 ** -24 * size
         rel = math.expm1(2 * e) + 2.0 ** -20
-        p_round = 2.0 ** -8 if self.dtype == BF16 else 2.0 ** -11
+        # P is rounded to bf16 for a bf16 cache and in the prefill kernel, else to f16
+        p_round = 2.0 ** -8 if self.dtype == BF16 or self.q.shape[2] > 1 else 2.0 ** -11
         tol = 2.0 ** -8 * want.abs() + (p_round + rel) * 1.01 * spread + 1e-30
         err = (out.double() - want).abs()
         assert torch.isfinite(out).all()
@@ -115,8 +118,9 @@ class Cache:
             return
         for s, n in enumerate(lens):
             got = self.w[s, :, :n].double() - before[s, :, :n].double()
-            # one rounding of the accumulator, and one for each term of the sum
-            tol = rel * 1.01 * ww[s] + 2.0 ** -24 * (self.w[s, :, :n].double().abs() + before[s, :, :n].double())
+            # the exponent's rounding, the sum's terms (within 2^-20), the accumulator's rounding
+            rel_w = rel + 2.0 ** -23 * (1.4427 * size + math.log2(max(n, 2)))
+            tol = rel_w * 1.01 * ww[s] + 2.0 ** -24 * (self.w[s, :, :n].double().abs() + before[s, :, :n].double())
             err = (got - ww[s]).abs()
             assert (err <= tol).all(), f"weights of {s}: {float((err / tol).max()):.2f} of the bound"
             assert torch.equal(self.w[s, :, n:], before[s, :, n:]), "weights past the sequence changed"
@@ -292,6 +296,90 @@ def test_decode_on_another_stream_and_in_two_graphs():
     o = a.run(False, stream=s)
     s.synchronize()
     assert torch.equal(o, want[0][0])
+
+
+PROMPTS = [
+    # q_len, lens, H, H_kv, page, block
+    (2, [2, 3, 40], 2, 1, 16, 16),
+    (5, [5, 129, 64], 4, 4, 32, 16),
+    (128, [128, 256, 200], 4, 2, 64, 64),
+    (129, [129, 1000], 6, 2, 16, 16),
+    (257, [300, 257], 3, 1, 256, 64),
+    (300, [2051], 8, 2, 128, 32),
+    (700, [5000, 701], 2, 2, 256, 256),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_many_query_rows(dtype, case, causal):
+    q_len, lens, H, H_kv, ps, bt = PROMPTS[case]
+    c = Cache(dtype, lens, H, H_kv, ps, bt, q_len=q_len, seed=20 + case, q_mul=2.0)
+    if dtype != BF16:
+        c.check(c.run(False, causal=causal), causal=causal)
+    before = c.w.clone()
+    out = c.run(True, causal=causal, max_len=max(lens) + 3)
+    c.check(out, before, causal=causal)
+    if dtype == BF16:           # the same kernel as without weights, to the bit
+        plain = api.paged(c.q, c.k, c.v, c.table, c.len_t, ps, causal, c.scale, max(lens))
+        assert torch.equal(plain, out)
+    w = c.w.clone()
+    c.w = before.clone()
+    c.run(True, causal=causal, max_len=max(lens) + 3)
+    assert torch.equal(c.w, w)
+
+
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("climb", [7.5, 40.0])
+def test_many_query_rows_with_climbing_scores(dtype, climb):
+    """Every 64-token block scores `climb` (base-2 units) above the last."""
+    n = 64 * 12
+    c = Cache(dtype, [n], 2, 1, 64, 64, q_len=200, seed=3)
+    c.q.zero_()
+    c.q[..., 0] = 4.0
+    raw(c.k)[..., 0] = raw(torch.tensor(64.0).to(dtype)[None]).to(DEV)
+    step = climb * math.log(2) / (4.0 * c.scale)
+    for i in range(12):
+        page = int(c.table[0, i])
+        if dtype == BF16:
+            c.k[page, :, :, 0] = (i - 6) * step
+        else:
+            c.ks[page] = max(i, 0.01) * step / 64
+    before = c.w.clone()
+    c.check(c.run(True), before)
+
+
+@pytest.mark.parametrize("ps", [16, 128])
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+def test_many_query_rows_leave_out_bad_pages(dtype, ps):
+    c = Cache(dtype, [700, 300], 4, 2, ps, 16, q_len=90, seed=21)
+    c.table[0, 2] = -1
+    c.table[1, 0] = 1 << 20
+    before = c.w.clone()
+    out = c.run(True)
+    assert clean() == B.PKV_DEVERR_BAD_PAGE
+    c.check(out, before)
+    assert torch.equal(c.w[0, :, 2 * ps:3 * ps], before[0, :, 2 * ps:3 * ps])
+
+
+@pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_nan_behind_the_causal_mask_stays_there(dtype, which):
+    """A block whose scale is NaN reaches the rows that see it and no others, within one tile."""
+    c = Cache(dtype, [100], 2, 1, 16, 16, q_len=100, seed=22)
+    getattr(c, which)[int(c.table[0, 3]), 0, 0] = float("nan")       # keys 48 .. 63
+    out = c.run(False)
+    assert torch.isfinite(out[0, :, :48]).all() and torch.isnan(out[0, :, 48:]).all()
+
+
+def test_more_query_rows_than_keys_is_flagged():
+    c = Cache(I8, [200, 50], 4, 2, 16, 16, q_len=60, seed=23)
+    before = c.w.clone()
+    out = c.run(True)
+    assert clean() == B.PKV_DEVERR_BAD_LEN
+    c.check(out, before)
+    assert (out[1, :, :10] == 0).all()            # rows before the first key see nothing
 
 
 # ---------------------------------------------------------------------- the write side --
