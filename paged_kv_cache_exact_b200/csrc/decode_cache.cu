@@ -37,11 +37,19 @@
 // units) go to the workspace and a second kernel turns them into weights once
 // the splits are merged: each (sequence, kv head, token) is owned by one
 // thread, so there are no atomics and the sums have one order.
+#include <mutex>
+
 #include "cache_attn.cuh"
+#include "cp_async.cuh"
 #include "q8.cuh"
+#include "sm100_ptx.cuh"
 
 namespace pkv {
 namespace {
+
+using sm100::f2;
+using sm100::fma2;
+using sm100::unf2;
 
 constexpr int D = 128;
 constexpr int kWarps = 4;
@@ -97,40 +105,44 @@ PKV_DEVINLINE void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
+// A load under a predicate that leaves the registers alone where it is false: a
+// plain conditional would put a wait for the load right behind it.
+PKV_DEVINLINE void load16_if(bool pred, const void* at, uint4& x) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w) : "l"(at), "r"((int)pred));
+}
+
 template <int kCache>
 struct Layout {
   static constexpr bool kBf16 = kCache == PKV_BF16;
   static constexpr int kRowBytes = D * (kBf16 ? 2 : 1);
-  static constexpr int kVec = kBf16 ? 8 : 4;      // 16-byte loads per lane, chunk and matrix
-  static constexpr int kDepth = kBf16 ? 1 : 2;    // chunks in registers per warp
+  static constexpr int kVec = kBf16 ? 8 : 4;                // 16-byte pieces per lane, chunk and matrix
+  static constexpr bool kRing = !kBf16;                     // chunks wait in shared memory, or in registers
+  static constexpr int kStages = kBf16 ? 1 : 3;             // chunks in flight per warp
+  static constexpr int kStageBytes = 2 * kVec * 32 * 16;    // K, then V: 4 or 8 KB
+  static constexpr int kRingBytes = kRing ? kWarps * kStages * kStageBytes : kWarps * 16 * D * 4;
   static constexpr float kLift = kBf16 ? 0.f : 7.f;
 };
 
-// Registers of one chunk of 16 tokens.
-template <int kCache>
-struct Chunk {
-  uint4 k[Layout<kCache>::kVec], v[Layout<kCache>::kVec];
-  float ks, vs;
-  int tok;           // first token
-  bool page_ok;
-};
-
 template <int kCache, int NT, bool kWeights>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 && kCache != PKV_BF16 ? 4 : 3)
 cache_decode_kernel(const CacheAttnParams p) {
   using Lay = Layout<kCache>;
   constexpr bool kBf16 = Lay::kBf16;
   constexpr int kHeads = 8 * NT;
+  extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][piece][lane] 16 bytes
   __shared__ int s_pages[kMaxSplitPages];
-  __shared__ __align__(16) float s_o[kWarps][kHeads][D];
+  __shared__ float2 s_scale[kBf16 ? 1 : kMaxSplitTokens / 16];   // (ks, vs) of every chunk
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const int split = blockIdx.x, s = blockIdx.z;
+  const int split = blockIdx.y, s = blockIdx.z;
   const int group = p.H / p.H_kv;
   const int n_hg = (group + kHeads - 1) / kHeads;
-  const int kvh = blockIdx.y / n_hg;
-  const int hg0 = (blockIdx.y % n_hg) * kHeads;             // first head within the group
+  const int kvh = blockIdx.x / n_hg;
+  const int hg0 = (blockIdx.x % n_hg) * kHeads;             // first head within the group
   const int h0 = kvh * group + hg0;
   const int nh = min(kHeads, group - hg0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -139,7 +151,7 @@ cache_decode_kernel(const CacheAttnParams p) {
   int L = p.seq_lens[s];
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
   if (L < 1 || L > cap) {
-    if (split == 0 && blockIdx.y == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
+    if (split == 0 && blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
     L = max(0, min(L, cap));
   }
   if (L <= 0) {
@@ -216,9 +228,10 @@ cache_decode_kernel(const CacheAttnParams p) {
   }
   __syncthreads();                                           // s_pages ready
 
-  const size_t stride = (size_t)p.H_kv * Lay::kRowBytes;     // bytes between tokens of a page
-  const char* kbase = static_cast<const char*>(p.k_pages) + (size_t)kvh * Lay::kRowBytes;
-  const char* vbase = static_cast<const char*>(p.v_pages) + (size_t)kvh * Lay::kRowBytes;
+  const int stride = p.H_kv * Lay::kRowBytes;                // bytes between tokens of a page
+  // this lane's rows of K and its column of V
+  const char* kbase = static_cast<const char*>(p.k_pages) + (size_t)kvh * Lay::kRowBytes + g * stride + 16 * t4;
+  const char* vbase = static_cast<const char*>(p.v_pages) + (size_t)kvh * Lay::kRowBytes + 16 * g;
   const int pmask = p.page_size - 1;
   const int n_chunks = (t_end - t_begin + 15) >> 4;
 
@@ -228,35 +241,71 @@ cache_decode_kernel(const CacheAttnParams p) {
     ok = phys >= 0;
     return ((size_t)(ok ? phys : 0) << p.page_shift) + (tok & pmask);
   };
-  auto load_k = [&](Chunk<kCache>& x, int c) {
-    const size_t row = chunk_row(c, x.page_ok);
-    x.tok = t_begin + 16 * c;
-    if (x.page_ok) {
-      const char* r0 = kbase + (row + g) * stride + 16 * t4;
-      const char* r1 = r0 + 8 * stride;
-#pragma unroll
-      for (int i = 0; i < Lay::kVec / 2; ++i) {
-        x.k[i] = ldg_nc_v4(r0 + 64 * i);
-        x.k[Lay::kVec / 2 + i] = ldg_nc_v4(r1 + 64 * i);
-      }
-      if (!kBf16) x.ks = __ldg(p.k_scales + (row >> p.block_shift) * p.H_kv + kvh);
-    }
-  };
-  auto load_v = [&](Chunk<kCache>& x, int c) {
+  // Ring: copy chunk c's pieces of this lane into stage st (zeros for a chunk
+  // that is not there, a bad page, and V rows past the sequence, which may hold
+  // NaN).  A lane later reads exactly what it copied: its own wait is all it needs.
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                        warp * Lay::kStages * Lay::kStageBytes + lane * 16;
+  auto prefetch = [&](int c, int st) {
     bool ok;
     const size_t row = chunk_row(c, ok);
-    const int tok = t_begin + 16 * c;
-    // rows past the sequence hold anything, NaN too: they are taken as zero
+    const int left = t_end - t_begin - 16 * c;               // rows of the chunk within the sequence
+    const uint32_t dst = mine + st * Lay::kStageBytes;
+    const char* r0 = kbase + row * stride;
+#pragma unroll
+    for (int i = 0; i < Lay::kVec / 2; ++i) {
+      cp_async16(dst + i * 512, r0 + 64 * i, ok);
+      cp_async16(dst + (Lay::kVec / 2 + i) * 512, r0 + 8 * stride + 64 * i, ok);
+    }
+    const char* v0 = vbase + row * stride;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 2 * t4 + (i & 1) + 8 * (i >> 1);
-      const bool in = ok && tok + r < t_end;
-      const char* at = vbase + (row + r) * stride + 16 * g;
-      x.v[i] = in ? ldg_nc_v4(at) : make_uint4(0u, 0u, 0u, 0u);
-      if (kBf16) x.v[4 + i] = in ? ldg_nc_v4(at + 128) : make_uint4(0u, 0u, 0u, 0u);
+      const bool in = ok && r < left;
+      cp_async16(dst + (Lay::kVec + i) * 512, v0 + r * stride, in);
+      if (kBf16) cp_async16(dst + (Lay::kVec + 4 + i) * 512, v0 + r * stride + 128, in);
     }
-    if (!kBf16 && ok) x.vs = __ldg(p.v_scales + (row >> p.block_shift) * p.H_kv + kvh);
+    cp_async_commit();
   };
+  // Registers: the next chunk's K follows this chunk's scores, its V this chunk's
+  // output.  The last row of the sequence stands in for V rows past it (their
+  // weight is 0).
+  uint4 kx[Lay::kVec] = {}, vx[Lay::kVec] = {};
+  auto load_k = [&](int c) {
+    bool ok;
+    const char* r0 = kbase + chunk_row(c, ok) * stride;
+#pragma unroll
+    for (int i = 0; i < Lay::kVec / 2; ++i) {
+      load16_if(ok, r0 + 64 * i, kx[i]);
+      load16_if(ok, r0 + 8 * stride + 64 * i, kx[Lay::kVec / 2 + i]);
+    }
+  };
+  auto load_v = [&](int c) {
+    bool ok;
+    const char* v0 = vbase + chunk_row(c, ok) * stride;
+    const int last = t_end - t_begin - 16 * c - 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = min(2 * t4 + (i & 1) + 8 * (i >> 1), last);
+      load16_if(ok, v0 + r * stride, vx[i]);
+      if (kBf16) load16_if(ok, v0 + r * stride + 128, vx[4 + i]);
+    }
+  };
+  if (Lay::kRing) {
+#pragma unroll
+    for (int i = 0; i < Lay::kStages - 1; ++i) prefetch(warp + i * kWarps, i);
+  } else {
+    load_k(warp);
+    load_v(warp);
+  }
+  if (!kBf16) {
+    for (int c = tid; c < n_chunks; c += kThreads) {
+      bool ok;
+      const size_t at = (chunk_row(c, ok) >> p.block_shift) * p.H_kv + kvh;
+      if (ok) s_scale[c] = make_float2(p.k_scales[at], p.v_scales[at]);
+    }
+    __syncthreads();
+  }
 
   float o[NT][8][4];
   float m[NT][2], l[NT][2];
@@ -268,26 +317,30 @@ cache_decode_kernel(const CacheAttnParams p) {
     l[nt][0] = l[nt][1] = 0.f;
   }
 
-  Chunk<kCache> buf[Lay::kDepth];
+  int st = 0;
+  for (int c = warp; c < n_chunks; c += kWarps) {
+    {
+      if (Lay::kRing) {
+        prefetch(c + (Lay::kStages - 1) * kWarps, st == 0 ? Lay::kStages - 1 : st - 1);   // the stage before this one
+        cp_async_wait<Lay::kStages - 1>();
+        const uint4* stage = reinterpret_cast<const uint4*>(ring + (warp * Lay::kStages + st) * Lay::kStageBytes) + lane;
+        st = st == Lay::kStages - 1 ? 0 : st + 1;
 #pragma unroll
-  for (int b = 0; b < Lay::kDepth; ++b) {
-    load_k(buf[b], warp + b * kWarps);
-    load_v(buf[b], warp + b * kWarps);
-  }
-  for (int c0 = warp; c0 < n_chunks; c0 += kWarps * Lay::kDepth) {
+        for (int i = 0; i < Lay::kVec; ++i) kx[i] = stage[i * 32];
 #pragma unroll
-    for (int b = 0; b < Lay::kDepth; ++b) {
-      const int c = c0 + b * kWarps;
-      if (c >= n_chunks) break;
-      Chunk<kCache>& x = buf[b];
-      const int tok = x.tok;
-      const bool page_ok = x.page_ok;
+        for (int i = 0; i < Lay::kVec; ++i) vx[i] = stage[(Lay::kVec + i) * 32];
+      }
+      const int tok = t_begin + 16 * c;
+      const bool page_ok = s_pages[(tok >> p.page_shift) - lp0] >= 0;
+      const float2 scales = kBf16 || !page_ok ? make_float2(1.f, 1.f) : s_scale[c];
       // S^T = K Q^T
-      float sc[NT][4];
+      float sc[NT][4], sd[NT][4];                            // two chains of four steps
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
       if (page_ok) {
-        const uint32_t* kw = reinterpret_cast<const uint32_t*>(x.k);
+        const uint32_t* kw = reinterpret_cast<const uint32_t*>(kx);
 #pragma unroll
         for (int st = 0; st < 8; ++st) {
           uint32_t a0, a1, a2, a3;
@@ -300,11 +353,15 @@ cache_decode_kernel(const CacheAttnParams p) {
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816<!kBf16>(sc[nt], a0, a1, a2, a3, qb[nt][st][0], qb[nt][st][1]);
+            mma16816<!kBf16>((st & 1) ? sd[nt] : sc[nt], a0, a1, a2, a3, qb[nt][st][0], qb[nt][st][1]);
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
       }
-      const float ks = kBf16 ? 1.f : x.ks;
-      load_k(x, c + kWarps * Lay::kDepth);
+      if (!Lay::kRing) load_k(c + kWarps);
+      const float ks = scales.x;
 
       // scores of tokens g, g + 8 and heads 2 t4, 2 t4 + 1 in base-2 units
       const bool in0 = page_ok && tok + g < t_end, in1 = page_ok && tok + g + 8 < t_end;
@@ -374,9 +431,9 @@ cache_decode_kernel(const CacheAttnParams p) {
         pb[nt][1] = transpose8x8(kBf16 ? pack_bf16x2(p2, p3) : pack_f16x2(p2, p3));
       }
       // O^T += vs V^T P^T
-      const float vs = kBf16 || !page_ok ? 1.f : x.vs;
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(x.v);
+      const float vs = scales.y;
       if (page_ok) {
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vx);
         if (kBf16) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {                      // word i of rows 2t, 2t+1, 2t+8, 2t+9
@@ -404,16 +461,23 @@ cache_decode_kernel(const CacheAttnParams p) {
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 mma16816<true>(acc, a[2 * e], a[2 * e + 1], bq[2 * e], bq[2 * e + 1], pb[nt][0], pb[nt][1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) o[nt][2 * w + e][q] = fmaf(vs, acc[q], o[nt][2 * w + e][q]);
+                for (int q = 0; q < 4; q += 2) {
+                  float* oo = &o[nt][2 * w + e][q];
+                  unf2(fma2(f2(vs, vs), f2(acc[q], acc[q + 1]), f2(oo[0], oo[1])), oo[0], oo[1]);
+                }
               }
           }
         }
       }
-      load_v(x, c + kWarps * Lay::kDepth);
+      if (!Lay::kRing) load_v(c + kWarps);
     }
   }
+  if (Lay::kRing) cp_async_wait<0>();
+  __syncthreads();                                           // the rings become the merge buffer
 
   // merge the warps
+  float (*s_o)[kHeads][D] = reinterpret_cast<float (*)[kHeads][D]>(ring);
+  static_assert(kWarps * kHeads * D * 4 <= Lay::kRingBytes, "merge buffer");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -543,16 +607,35 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const Cac
   }
 }
 
+template <int kCache, int NT, bool kWeights>
+cudaError_t launch_split(const CacheAttnParams& p, dim3 grid, cudaStream_t stream) {
+  // The shared-memory limit is an attribute per device; host threads may get
+  // here at once, so the once-per-device record is kept under a lock.
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(cache_decode_kernel<kCache, NT, kWeights>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kCache>::kRingBytes);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  cache_decode_kernel<kCache, NT, kWeights><<<grid, kThreads, Layout<kCache>::kRingBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int kCache, bool kWeights>
 cudaError_t launch_decode(const CacheAttnParams& p, cudaStream_t stream) {
   const int group = p.H / p.H_kv;
   const int heads = group > 8 ? 16 : 8;
-  const dim3 grid(p.max_splits, p.H_kv * ((group + heads - 1) / heads), p.num_seqs);
-  if (group > 8)
-    cache_decode_kernel<kCache, 2, kWeights><<<grid, kThreads, 0, stream>>>(p);
-  else
-    cache_decode_kernel<kCache, 1, kWeights><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(p.H_kv * ((group + heads - 1) / heads), p.max_splits, p.num_seqs);
+  return group > 8 ? launch_split<kCache, 2, kWeights>(p, grid, stream)
+                   : launch_split<kCache, 1, kWeights>(p, grid, stream);
 }
 
 // The kernel after the split kernel, as its programmatic dependent: it may be
