@@ -105,33 +105,33 @@ PKV_DEVINLINE void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// A load under a predicate that leaves the registers alone where it is false: a
-// plain conditional would put a wait for the load right behind it.
-PKV_DEVINLINE void load16_if(bool pred, const void* at, uint4& x) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-      : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w) : "l"(at), "r"((int)pred));
-}
+// Where a 16-byte piece of a row lies in shared memory: pieces are permuted so
+// that the eight lanes of a fragment read meet eight different bank groups, K's
+// (two rows, four pieces) and V's (four rows, two pieces).
+PKV_DEVINLINE int k_swizzle(int row) { return (row & 1) << 2; }
+PKV_DEVINLINE int v_swizzle(int row) { return row & 6; }
 
 template <int kCache>
 struct Layout {
   static constexpr bool kBf16 = kCache == PKV_BF16;
   static constexpr int kRowBytes = D * (kBf16 ? 2 : 1);
   static constexpr int kVec = kBf16 ? 8 : 4;                // 16-byte pieces per lane, chunk and matrix
-  static constexpr bool kRing = !kBf16;                     // chunks wait in shared memory, or in registers
-  static constexpr int kStages = kBf16 ? 1 : 3;             // chunks in flight per warp
-  static constexpr int kStageBytes = 2 * kVec * 32 * 16;    // K, then V: 4 or 8 KB
-  static constexpr int kRingBytes = kRing ? kWarps * kStages * kStageBytes : kWarps * 16 * D * 4;
+  static constexpr int kRowLanes = kRowBytes / 16;          // lanes that copy a row
+  static constexpr int kUnroll = kBf16 ? 1 : 2;             // chunks a warp works on at once
+  static constexpr int kStages = 2;                         // ring depth, in steps of kUnroll chunks
+  static constexpr int kChunkBytes = 2 * kVec * 32 * 16;    // K, then V: 4 or 8 KB
+  static constexpr int kStageBytes = kUnroll * kChunkBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr float kLift = kBf16 ? 0.f : 7.f;
 };
 
 template <int kCache, int NT, bool kWeights>
-__global__ void __launch_bounds__(kThreads, NT == 1 && kCache != PKV_BF16 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 cache_decode_kernel(const CacheAttnParams p) {
   using Lay = Layout<kCache>;
   constexpr bool kBf16 = Lay::kBf16;
   constexpr int kHeads = 8 * NT;
+  constexpr int U = Lay::kUnroll;
   extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][piece][lane] 16 bytes
   __shared__ int s_pages[kMaxSplitPages];
   __shared__ float2 s_scale[kBf16 ? 1 : kMaxSplitTokens / 16];   // (ks, vs) of every chunk
@@ -229,9 +229,9 @@ cache_decode_kernel(const CacheAttnParams p) {
   __syncthreads();                                           // s_pages ready
 
   const int stride = p.H_kv * Lay::kRowBytes;                // bytes between tokens of a page
-  // this lane's rows of K and its column of V
-  const char* kbase = static_cast<const char*>(p.k_pages) + (size_t)kvh * Lay::kRowBytes + g * stride + 16 * t4;
-  const char* vbase = static_cast<const char*>(p.v_pages) + (size_t)kvh * Lay::kRowBytes + 16 * g;
+  // this lane's 16 bytes of a row in a copy
+  const char* kbase = static_cast<const char*>(p.k_pages) + (size_t)kvh * Lay::kRowBytes + 16 * (lane % Lay::kRowLanes);
+  const char* vbase = static_cast<const char*>(p.v_pages) + (size_t)kvh * Lay::kRowBytes + 16 * (lane % Lay::kRowLanes);
   const int pmask = p.page_size - 1;
   const int n_chunks = (t_end - t_begin + 15) >> 4;
 
@@ -241,63 +241,33 @@ cache_decode_kernel(const CacheAttnParams p) {
     ok = phys >= 0;
     return ((size_t)(ok ? phys : 0) << p.page_shift) + (tok & pmask);
   };
-  // Ring: copy chunk c's pieces of this lane into stage st (zeros for a chunk
-  // that is not there, a bad page, and V rows past the sequence, which may hold
-  // NaN).  A lane later reads exactly what it copied: its own wait is all it needs.
-  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
-                        warp * Lay::kStages * Lay::kStageBytes + lane * 16;
-  auto prefetch = [&](int c, int st) {
+  // Copy chunk c into the ring (zeros for a chunk that is not there, a bad page,
+  // and V rows past the sequence, which may hold NaN).  Consecutive lanes take
+  // consecutive bytes of a row: eight lanes make one 128-byte request, where a
+  // fragment's own order (four rows per eight lanes) would make four.
+  const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * Lay::kStages * Lay::kStageBytes;
+  constexpr int kRowsAtOnce = 32 / Lay::kRowLanes;
+  auto prefetch = [&](int c, uint32_t dst) {
     bool ok;
     const size_t row = chunk_row(c, ok);
     const int left = t_end - t_begin - 16 * c;               // rows of the chunk within the sequence
-    const uint32_t dst = mine + st * Lay::kStageBytes;
-    const char* r0 = kbase + row * stride;
-#pragma unroll
-    for (int i = 0; i < Lay::kVec / 2; ++i) {
-      cp_async16(dst + i * 512, r0 + 64 * i, ok);
-      cp_async16(dst + (Lay::kVec / 2 + i) * 512, r0 + 8 * stride + 64 * i, ok);
-    }
+    const char* k0 = kbase + row * stride;
     const char* v0 = vbase + row * stride;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * t4 + (i & 1) + 8 * (i >> 1);
-      const bool in = ok && r < left;
-      cp_async16(dst + (Lay::kVec + i) * 512, v0 + r * stride, in);
-      if (kBf16) cp_async16(dst + (Lay::kVec + 4 + i) * 512, v0 + r * stride + 128, in);
+    for (int i = 0; i < Lay::kVec; ++i) {
+      const int r = lane / Lay::kRowLanes + kRowsAtOnce * i, ch = lane % Lay::kRowLanes;
+      cp_async16(dst + r * Lay::kRowBytes + ((ch ^ k_swizzle(r)) << 4), k0 + r * stride, ok);
+      cp_async16(dst + Lay::kChunkBytes / 2 + r * Lay::kRowBytes + ((ch ^ v_swizzle(r)) << 4), v0 + r * stride,
+                 ok && r < left);
     }
+  };
+  auto prefetch_step = [&](int c, int st) {                  // chunks c, c + kWarps, ...
+#pragma unroll
+    for (int u = 0; u < U; ++u) prefetch(c + u * kWarps, mine + st * Lay::kStageBytes + u * Lay::kChunkBytes);
     cp_async_commit();
   };
-  // Registers: the next chunk's K follows this chunk's scores, its V this chunk's
-  // output.  The last row of the sequence stands in for V rows past it (their
-  // weight is 0).
-  uint4 kx[Lay::kVec] = {}, vx[Lay::kVec] = {};
-  auto load_k = [&](int c) {
-    bool ok;
-    const char* r0 = kbase + chunk_row(c, ok) * stride;
 #pragma unroll
-    for (int i = 0; i < Lay::kVec / 2; ++i) {
-      load16_if(ok, r0 + 64 * i, kx[i]);
-      load16_if(ok, r0 + 8 * stride + 64 * i, kx[Lay::kVec / 2 + i]);
-    }
-  };
-  auto load_v = [&](int c) {
-    bool ok;
-    const char* v0 = vbase + chunk_row(c, ok) * stride;
-    const int last = t_end - t_begin - 16 * c - 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = min(2 * t4 + (i & 1) + 8 * (i >> 1), last);
-      load16_if(ok, v0 + r * stride, vx[i]);
-      if (kBf16) load16_if(ok, v0 + r * stride + 128, vx[4 + i]);
-    }
-  };
-  if (Lay::kRing) {
-#pragma unroll
-    for (int i = 0; i < Lay::kStages - 1; ++i) prefetch(warp + i * kWarps, i);
-  } else {
-    load_k(warp);
-    load_v(warp);
-  }
+  for (int i = 0; i < Lay::kStages - 1; ++i) prefetch_step(warp + i * kWarps * U, i);
   if (!kBf16) {
     for (int c = tid; c < n_chunks; c += kThreads) {
       bool ok;
@@ -318,161 +288,187 @@ cache_decode_kernel(const CacheAttnParams p) {
   }
 
   int st = 0;
-  for (int c = warp; c < n_chunks; c += kWarps) {
-    {
-      if (Lay::kRing) {
-        prefetch(c + (Lay::kStages - 1) * kWarps, st == 0 ? Lay::kStages - 1 : st - 1);   // the stage before this one
-        cp_async_wait<Lay::kStages - 1>();
-        const uint4* stage = reinterpret_cast<const uint4*>(ring + (warp * Lay::kStages + st) * Lay::kStageBytes) + lane;
-        st = st == Lay::kStages - 1 ? 0 : st + 1;
+  for (int c = warp; c < n_chunks; c += kWarps * U) {
+    __syncwarp();                                            // every lane has read the stage that is refilled now
+    prefetch_step(c + (Lay::kStages - 1) * kWarps * U, st == 0 ? Lay::kStages - 1 : st - 1);
+    cp_async_wait<Lay::kStages - 1>();
+    __syncwarp();                                            // every lane's copies have landed
+    const uint8_t* stage = ring + (warp * Lay::kStages + st) * Lay::kStageBytes;
+    st = st == Lay::kStages - 1 ? 0 : st + 1;
+    // K: rows g and g + 8, 16-byte pieces t4, t4 + 4, ...; V: piece g (and g + 8)
+    // of rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
+    uint4 kx[U][Lay::kVec], vx[U][Lay::kVec];
 #pragma unroll
-        for (int i = 0; i < Lay::kVec; ++i) kx[i] = stage[i * 32];
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* kc = stage + u * Lay::kChunkBytes;
+      const uint8_t* vc = kc + Lay::kChunkBytes / 2;
 #pragma unroll
-        for (int i = 0; i < Lay::kVec; ++i) vx[i] = stage[(Lay::kVec + i) * 32];
+      for (int i = 0; i < Lay::kVec / 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = g + 8 * e;
+          kx[u][e * (Lay::kVec / 2) + i] =
+              *reinterpret_cast<const uint4*>(kc + r * Lay::kRowBytes + (((4 * i + t4) ^ k_swizzle(r)) << 4));
+        }
+#pragma unroll
+      for (int i = 0; i < Lay::kVec; ++i) {
+        const int r = 2 * t4 + (i & 1) + 8 * ((i >> 1) & 1);
+        vx[u][i] = *reinterpret_cast<const uint4*>(vc + r * Lay::kRowBytes + (((g + 8 * (i >> 2)) ^ v_swizzle(r)) << 4));
       }
-      const int tok = t_begin + 16 * c;
-      const bool page_ok = s_pages[(tok >> p.page_shift) - lp0] >= 0;
-      const float2 scales = kBf16 || !page_ok ? make_float2(1.f, 1.f) : s_scale[c];
-      // S^T = K Q^T
-      float sc[NT][4], sd[NT][4];                            // two chains of four steps
+    }
+    int tok[U];
+    bool page_ok[U];
+    float2 scales[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int cu = c + u * kWarps;
+      tok[u] = t_begin + 16 * cu;
+      page_ok[u] = cu < n_chunks && s_pages[(tok[u] >> p.page_shift) - lp0] >= 0;
+      scales[u] = kBf16 || !page_ok[u] ? make_float2(1.f, 1.f) : s_scale[kBf16 ? 0 : cu];
+    }
+    // S^T = K Q^T, in two chains of four steps
+    float sc[U][NT][4], sd[U][NT][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nt][e] = sd[nt][e] = 0.f;
-      if (page_ok) {
-        const uint32_t* kw = reinterpret_cast<const uint32_t*>(kx);
+        for (int e = 0; e < 4; ++e) sc[u][nt][e] = sd[u][nt][e] = 0.f;
 #pragma unroll
-        for (int st = 0; st < 8; ++st) {
-          uint32_t a0, a1, a2, a3;
-          if (kBf16) {
-            a0 = kw[2 * st], a2 = kw[2 * st + 1];
-            a1 = kw[16 + 2 * st], a3 = kw[16 + 2 * st + 1];
-          } else {
-            codes_to_f16<kCache>(kw[st], a0, a2);
-            codes_to_f16<kCache>(kw[8 + st], a1, a3);
-          }
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816<!kBf16>((st & 1) ? sd[nt] : sc[nt], a0, a1, a2, a3, qb[nt][st][0], qb[nt][st][1]);
+      for (int u = 0; u < U; ++u) {
+        const uint32_t* kw = reinterpret_cast<const uint32_t*>(kx[u]);
+        uint32_t a0, a1, a2, a3;
+        if (kBf16) {
+          a0 = kw[2 * i], a2 = kw[2 * i + 1];
+          a1 = kw[16 + 2 * i], a3 = kw[16 + 2 * i + 1];
+        } else {
+          codes_to_f16<kCache>(kw[i], a0, a2);
+          codes_to_f16<kCache>(kw[8 + i], a1, a3);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
+          mma16816<!kBf16>((i & 1) ? sd[u][nt] : sc[u][nt], a0, a1, a2, a3, qb[nt][i][0], qb[nt][i][1]);
       }
-      if (!Lay::kRing) load_k(c + kWarps);
-      const float ks = scales.x;
 
-      // scores of tokens g, g + 8 and heads 2 t4, 2 t4 + 1 in base-2 units
-      const bool in0 = page_ok && tok + g < t_end, in1 = page_ok && tok + g + 8 < t_end;
-      bool passed = false;
+    // scores of tokens g, g + 8 and heads 2 t4, 2 t4 + 1 in base-2 units
+    bool passed = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in0 = page_ok[u] && tok[u] + g < t_end, in1 = page_ok[u] && tok[u] + g + 8 < t_end;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = hm[nt][0] * ks, f1 = hm[nt][1] * ks;
-        sc[nt][0] = in0 ? sc[nt][0] * f0 : -INFINITY;
-        sc[nt][1] = in0 ? sc[nt][1] * f1 : -INFINITY;
-        sc[nt][2] = in1 ? sc[nt][2] * f0 : -INFINITY;
-        sc[nt][3] = in1 ? sc[nt][3] * f1 : -INFINITY;
-        passed = passed || fmaxf(sc[nt][0], sc[nt][2]) > m[nt][0] + (Lay::kLift + 8.f) ||
-                 fmaxf(sc[nt][1], sc[nt][3]) > m[nt][1] + (Lay::kLift + 8.f);
+        const float f0 = hm[nt][0] * scales[u].x, f1 = hm[nt][1] * scales[u].x;
+        float (&x)[4] = sc[u][nt];
+        x[0] = in0 ? (x[0] + sd[u][nt][0]) * f0 : -INFINITY;
+        x[1] = in0 ? (x[1] + sd[u][nt][1]) * f1 : -INFINITY;
+        x[2] = in1 ? (x[2] + sd[u][nt][2]) * f0 : -INFINITY;
+        x[3] = in1 ? (x[3] + sd[u][nt][3]) * f1 : -INFINITY;
+        passed = passed || fmaxf(x[0], x[2]) > m[nt][0] + (Lay::kLift + 8.f) ||
+                 fmaxf(x[1], x[3]) > m[nt][1] + (Lay::kLift + 8.f);
       }
       if (kWeights) {
         // [S, H_kv, tokens, group]; tokens past the sequence are not written
-        float* lg = p.logits + (((size_t)s * p.H_kv + kvh) * p.logit_tokens + tok + g) * group + hg0 + 2 * t4;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool in = tok + g + 8 * e < t_end;
-            float* at = lg + (size_t)(8 * e) * group + 8 * nt;
-            if ((group & 1) == 0) {
-              if (in && 8 * nt + 2 * t4 < nh)
-                *reinterpret_cast<float2*>(at) = make_float2(sc[nt][2 * e], sc[nt][2 * e + 1]);
-            } else {
-              if (in && 8 * nt + 2 * t4 < nh) at[0] = sc[nt][2 * e];
-              if (in && 8 * nt + 2 * t4 + 1 < nh) at[1] = sc[nt][2 * e + 1];
-            }
-          }
-        }
-      }
-      if (__any_sync(0xffffffffu, passed)) {
+        float* lg = p.logits + (((size_t)s * p.H_kv + kvh) * p.logit_tokens + tok[u] + g) * group + hg0 + 2 * t4;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float mx = fmaxf(sc[nt][j], sc[nt][2 + j]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            if (mx > m[nt][j] + (Lay::kLift + 8.f)) {
-              const float mn = mx - Lay::kLift;
-              const float a = ex2(m[nt][j] - mn);            // from -inf: 0
-              m[nt][j] = mn;
-              l[nt][j] *= a;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                o[nt][i][j] *= a;
-                o[nt][i][2 + j] *= a;
-              }
+          for (int e = 0; e < 2; ++e) {
+            const bool in = tok[u] + g + 8 * e < t_end;
+            float* at = lg + (size_t)(8 * e) * group + 8 * nt;
+            if ((group & 1) == 0) {
+              if (in && 8 * nt + 2 * t4 < nh)
+                *reinterpret_cast<float2*>(at) = make_float2(sc[u][nt][2 * e], sc[u][nt][2 * e + 1]);
+            } else {
+              if (in && 8 * nt + 2 * t4 < nh) at[0] = sc[u][nt][2 * e];
+              if (in && 8 * nt + 2 * t4 + 1 < nh) at[1] = sc[u][nt][2 * e + 1];
             }
           }
       }
-      // P^T as the B operand: column n = head, rows = the chunk's tokens
-      uint32_t pb[NT][2];
+    }
+    if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-        const float p0 = ex2(sc[nt][0] - s0), p1 = ex2(sc[nt][1] - s1);
-        const float p2 = ex2(sc[nt][2] - s0), p3 = ex2(sc[nt][3] - s1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pb[nt][0] = transpose8x8(kBf16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1));
-        pb[nt][1] = transpose8x8(kBf16 ? pack_bf16x2(p2, p3) : pack_f16x2(p2, p3));
-      }
-      // O^T += vs V^T P^T
-      const float vs = scales.y;
-      if (page_ok) {
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vx);
-        if (kBf16) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {                      // word i of rows 2t, 2t+1, 2t+8, 2t+9
-            const int b0 = (i >> 2) * 16 + (i & 3);
-            const uint32_t r0 = vw[b0], r1 = vw[b0 + 4], r2 = vw[b0 + 8], r3 = vw[b0 + 12];
-            const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
-            const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+        for (int j = 0; j < 2; ++j) {
+          float mx = fmaxf(sc[0][nt][j], sc[0][nt][2 + j]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816<false>(o[nt][i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          }
-        } else {
+          for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][j], sc[u][nt][2 + j]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (mx > m[nt][j] + (Lay::kLift + 8.f)) {
+            const float mn = mx - Lay::kLift;
+            const float a = ex2(m[nt][j] - mn);              // from -inf: 0
+            m[nt][j] = mn;
+            l[nt][j] *= a;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            // bytes 4w .. 4w+3 of rows (2t, 2t+1) and (2t+8, 2t+9), interleaved by row
-            uint32_t a[4], bq[4];
-            codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x5140), a[0], a[1]);
-            codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x7362), a[2], a[3]);
-            codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x5140), bq[0], bq[1]);
-            codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x7362), bq[2], bq[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {                  // tile 2w + e: head dims 16 g + 4w + 2e, + 1
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816<true>(acc, a[2 * e], a[2 * e + 1], bq[2 * e], bq[2 * e + 1], pb[nt][0], pb[nt][1]);
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                  float* oo = &o[nt][2 * w + e][q];
-                  unf2(fma2(f2(vs, vs), f2(acc[q], acc[q + 1]), f2(oo[0], oo[1])), oo[0], oo[1]);
-                }
-              }
+            for (int i = 0; i < 8; ++i) {
+              o[nt][i][j] *= a;
+              o[nt][i][2 + j] *= a;
+            }
           }
         }
+    }
+    // P^T as the B operand: column n = head, rows = the chunk's tokens
+    uint32_t pb[U][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+      const float s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float p0 = ex2(sc[u][nt][0] - s0), p1 = ex2(sc[u][nt][1] - s1);
+        const float p2 = ex2(sc[u][nt][2] - s0), p3 = ex2(sc[u][nt][3] - s1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        pb[u][nt][0] = transpose8x8(kBf16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1));
+        pb[u][nt][1] = transpose8x8(kBf16 ? pack_bf16x2(p2, p3) : pack_f16x2(p2, p3));
       }
-      if (!Lay::kRing) load_v(c + kWarps);
+    }
+    // O^T += vs V^T P^T
+    if (kBf16) {
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(vx[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                          // word i of rows 2t, 2t+1, 2t+8, 2t+9
+        const int b0 = (i >> 2) * 16 + (i & 3);
+        const uint32_t r0 = vw[b0], r1 = vw[b0 + 4], r2 = vw[b0 + 8], r3 = vw[b0 + 12];
+        const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
+        const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816<false>(o[nt][i], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+      }
+    } else {
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // bytes 4w .. 4w+3 of rows (2t, 2t+1) and (2t+8, 2t+9), interleaved by row
+          const uint32_t* vw = reinterpret_cast<const uint32_t*>(vx[u]);
+          const float vs = scales[u].y;
+          uint32_t a[4], b[4];
+          codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x5140), a[0], a[1]);
+          codes_to_f16<kCache>(__byte_perm(vw[w], vw[4 + w], 0x7362), a[2], a[3]);
+          codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x5140), b[0], b[1]);
+          codes_to_f16<kCache>(__byte_perm(vw[8 + w], vw[12 + w], 0x7362), b[2], b[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {                    // tile 2w + e: head dims 16 g + 4w + 2e, + 1
+              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<true>(acc, a[2 * e], a[2 * e + 1], b[2 * e], b[2 * e + 1], pb[u][nt][0], pb[u][nt][1]);
+#pragma unroll
+              for (int q = 0; q < 4; q += 2) {
+                float* oo = &o[nt][2 * w + e][q];
+                unf2(fma2(f2(vs, vs), f2(acc[q], acc[q + 1]), f2(oo[0], oo[1])), oo[0], oo[1]);
+              }
+            }
+        }
     }
   }
-  if (Lay::kRing) cp_async_wait<0>();
+  cp_async_wait<0>();
   __syncthreads();                                           // the rings become the merge buffer
 
   // merge the warps
@@ -662,8 +658,12 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
   const int heads = group > 8 ? 16 : 8;
   const long long pairs = (long long)num_seqs * H_kv * ((group + heads - 1) / heads);
   int st = 64 < page_size ? page_size : 64;
-  // double while at least 8 CTAs per SM remain
-  while (st < kMaxSplitTokens && pairs * ((max_seq_len + 2LL * st - 1) / (2LL * st)) >= 148LL * 8) st *= 2;
+  // Double while at least 8 CTAs per SM remain.  A split writes (and the merge
+  // reads) 512 bytes per query head: with few heads that is little, and shorter
+  // splits balance ragged lengths better (64 sequences x 32 heads, int8: 441 us at
+  // 1024 tokens, 455 at 4096; 16 long ones x 8 heads a kv head: 141 and 137 us).
+  const int most = group >= 4 ? kMaxSplitTokens : 1024;
+  while (st < most && pairs * ((max_seq_len + 2LL * st - 1) / (2LL * st)) >= 148LL * 8) st *= 2;
   while (((long long)max_seq_len + st - 1) / st > kMaxSplits && st < kMaxSplitTokens) st *= 2;
   *split_tokens = st;
   *max_splits = (int)(((long long)max_seq_len + st - 1) / st);
