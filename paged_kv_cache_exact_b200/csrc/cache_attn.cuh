@@ -70,7 +70,7 @@ struct EvictParams {
   float2* block_scale;         // [S, H_kv, max_blocks]: new (k, v) scale of every block
   unsigned int* err;
   int num_seqs, H_kv, num_pages, page_size, page_shift, block_shift, max_pages, max_seq_len;
-  int budget, recent, weights_stride, row_bytes, max_blocks, cache_dtype;
+  int budget, recent, weights_stride, row_bytes, slice_bytes, max_blocks, cache_dtype;   // slice_bytes: set by the launcher
 };
 
 // Split plan of single-token attention: tokens a split, splits of the longest sequence.

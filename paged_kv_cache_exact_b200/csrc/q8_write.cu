@@ -14,11 +14,14 @@
 // does not depend on how a prompt was cut into calls other than through the
 // definition above.
 //
-// One CTA per (block, call): the block's rows of every head, K and V.  A warp
-// owns one (head, K or V) at a time: lane i holds elements 4i .. 4i+3 of a
-// row, so a row of new values is one 256-byte load, its codes one 128-byte
-// store, and the maximum one shuffle reduction per block.  The bound is HBM:
-// 2 bytes read and 1 written per element.
+// One CTA per (block of the call, a few of the 2 H_kv (head, K or V) pairs): a warp
+// takes 16 of a pair's rows, so a 16-token block has 8 pairs a CTA and a 128-token
+// block one.  Lane i holds elements 4i .. 4i+3 of a row, so a row of new values is
+// one 256-byte load and its codes one 128-byte store.  The rows stay in registers
+// between the maximum and the rounding (in a 256-token block a warp has 32 rows
+// and reads the second 16 again, from L2).  The bound is HBM: 2 bytes read and 1
+// written per element; the chain table -> rows -> scale -> codes is hidden by the
+// other CTAs of the SM.
 #include "cache_attn.cuh"
 #include "q8.cuh"
 
@@ -28,6 +31,7 @@ namespace {
 constexpr int D = 128;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kHeld = 16;            // rows a warp takes
 
 // Four consecutive elements of a new row as stored (bf16 or f32).
 template <typename T> struct Row4;
@@ -63,17 +67,18 @@ template <> struct Row4<float> {
 // items from cu_new[s] / block + 2 s on, which leaves room for every block its
 // rows can touch: n rows touch at most floor(n / block) + 2 blocks.
 template <int kCache, typename T>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const AppendQ8Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_kernel(const AppendQ8Params p) {
   __shared__ int s_row0, s_rows, s_off, s_dst;
-  if (threadIdx.x == 0) {
-    const int item = blockIdx.x;
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((p.cu_new[mid] >> p.block_shift) + 2 * mid <= item) lo = mid; else hi = mid - 1;
-    }
-    const int s = lo;
-    const int c0 = p.cu_new[s], n = p.cu_new[s + 1] - c0;
+  __shared__ uint32_t s_max[kWarps];
+  if (threadIdx.x == 0) s_rows = 0;
+  __syncthreads();
+  // The thread whose sequence has this item looks the block up: a search by one
+  // thread would be a chain of dependent loads.
+  const int item = blockIdx.x;
+  for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
+    const int c0 = p.cu_new[s], c1 = p.cu_new[s + 1];
+    if (item < (c0 >> p.block_shift) + 2 * s || item >= (c1 >> p.block_shift) + 2 * s + 2) continue;
+    const int n = c1 - c0;
     const int start = p.start_pos[s];
     const int k = item - ((c0 >> p.block_shift) + 2 * s);        // k-th block of this sequence's rows
     const int bt = 1 << p.block_shift;
@@ -102,15 +107,22 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const AppendQ8Param
         }
       }
     }
-    s_rows = rows, s_row0 = row0, s_off = off, s_dst = dst;
+    s_row0 = row0, s_off = off, s_dst = dst;
+    s_rows = dst < 0 ? 0 : rows;
   }
   __syncthreads();
-  const int rows = s_rows, row0 = s_row0, off = s_off, dst = s_dst;
-  if (rows == 0 || dst < 0) return;
+  const int rows = s_rows;
+  if (rows == 0) return;
+  const int row0 = s_row0, off = s_off, dst = s_dst;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int pair = warp; pair < 2 * p.H_kv; pair += kWarps) {
-    const int h = pair >> 1;
+  const int bt = 1 << p.block_shift;
+  const int parts = min(kWarps, bt / kHeld);                       // warps a pair
+  const int pair = blockIdx.y * (kWarps / parts) + warp / parts;
+  const int part = warp % parts;
+  const bool live = pair < 2 * p.H_kv;
+  {
+    const int h = live ? pair >> 1 : 0;
     const void* src = (pair & 1) ? p.v_new : p.k_new;
     uint8_t* pages = static_cast<uint8_t*>((pair & 1) ? p.v_pages : p.k_pages);
     float* scale = ((pair & 1) ? p.v_scales : p.k_scales) + (size_t)dst * p.H_kv + h;
@@ -119,38 +131,59 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const AppendQ8Param
     const size_t code_stride = (size_t)p.H_kv * D / 4;              // words between tokens
 
     uint32_t m = 0;
+    Row4<T> x[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {                               // rows part, part + parts, ...
+      const int r = part + i * parts;
+      if (live && r < rows) x[i].load(src, src_row + (size_t)r * p.H_kv, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (live && part + i * parts < rows) m = max(m, x[i].amax());
 #pragma unroll 8
-    for (int r = 0; r < rows; ++r) {
-      Row4<T> x;
-      x.load(src, src_row + (size_t)r * p.H_kv, lane);
-      m = max(m, x.amax());
+    for (int r = part + kHeld * parts; r < rows; r += parts) {
+      Row4<T> y;
+      if (live) y.load(src, src_row + (size_t)r * p.H_kv, lane), m = max(m, y.amax());
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    const float old = off > 0 ? *scale : 0.f;
+    if (parts > 1) {
+      if (lane == 0) s_max[warp] = m;
+    }
+    const float was = live && off > 0 ? *scale : 0.f;
+    __syncthreads();                                                // the maxima are there, the old scale is read
+    if (!live) return;
+    if (parts > 1)
+      for (int i = 0; i < parts; ++i) m = max(m, s_max[warp - part + i]);
+    const float old = was;
     const bool broken = m >= 0x7f800000u || isnan(old);             // NaN or infinity: the block reads NaN
     const float s = broken ? __uint_as_float(0x7fffffffu)
                            : fmaxf(fmaxf(old, __fdiv_rn(__uint_as_float(m), code_max<kCache>())), kMinScale);
-    __syncwarp();                                                   // every lane has read the old scale
-    if (lane == 0) *scale = s;
+    if (lane == 0 && part == 0) *scale = s;
     if (off > 0 && s > old) {
       const float ratio = __fdiv_rn(old, s);
-      for (int r = 0; r < off; ++r)
+#pragma unroll 4
+      for (int r = part; r < off; r += parts)
         code[r * code_stride] = requantize4<kCache>(code[r * code_stride], ratio, old, s);
     }
     const float inv = __fdiv_rn(1.f, s);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      Row4<T> x;
-      x.load(src, src_row + (size_t)r * p.H_kv, lane);
-      uint32_t w = 0;
+    auto store = [&](int r, const Row4<T>& y) {
+      float q[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float v = x.at(i);
-        w |= code_of<kCache>(v * inv, [&] {
-               return code_exact<kCache>(static_cast<double>(v), static_cast<double>(s));
-             }) << (8 * i);
-      }
+      for (int i = 0; i < 4; ++i) q[i] = y.at(i) * inv;
+      const uint32_t w = codes_of4<kCache>(q, [&](int i) {
+        const float v = i == 0 ? y.at(0) : i == 1 ? y.at(1) : i == 2 ? y.at(2) : y.at(3);
+        return code_exact<kCache>(static_cast<double>(v), static_cast<double>(s));
+      });
       code[(size_t)(off + r) * code_stride] = broken ? 0u : w;
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (part + i * parts < rows) store(part + i * parts, x[i]);
+#pragma unroll 4
+    for (int r = part + kHeld * parts; r < rows; r += parts) {
+      Row4<T> y;
+      y.load(src, src_row + (size_t)r * p.H_kv, lane);
+      store(r, y);
     }
   }
 }
@@ -183,7 +216,11 @@ __global__ void __launch_bounds__(kThreads) copy_pages_q8_kernel(const CopyPages
 cudaError_t launch_append_q8(const AppendQ8Params& p, cudaStream_t stream) {
   const long long items = ((long long)p.num_new >> p.block_shift) + 2LL * p.num_seqs;
   if (items > 0x7fffffffLL) return cudaErrorNotSupported;
-  const unsigned grid = (unsigned)items;
+  const int parts = (1 << p.block_shift) / kHeld < kWarps ? (1 << p.block_shift) / kHeld : kWarps;
+  const int pairs = kWarps / parts;                                // (head, K or V) pairs a CTA
+  const long long groups = (2LL * p.H_kv + pairs - 1) / pairs;
+  if (groups > 65535) return cudaErrorNotSupported;
+  const dim3 grid((unsigned)items, (unsigned)groups);
   if (p.cache_dtype == PKV_I8) {
     if (p.rows_f32) append_q8_kernel<PKV_I8, float><<<grid, kThreads, 0, stream>>>(p);
     else append_q8_kernel<PKV_I8, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);

@@ -69,11 +69,12 @@ PKV_DEVINLINE void load_row16(const char* row, int c, uint4& a, uint4& b) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)                                  // codes are exact in bf16
-        o[2 * i + e] = pack_bf16x2(code_value<kCache>((w[i] >> (16 * e)) & 0xffu),
-                                   code_value<kCache>((w[i] >> (16 * e + 8)) & 0xffu));
+    for (int i = 0; i < 4; ++i) {                                  // codes are exact in bf16
+      float v[4];
+      values_of4<kCache>(w[i], v);
+      o[2 * i] = pack_bf16x2(v[0], v[1]);
+      o[2 * i + 1] = pack_bf16x2(v[2], v[3]);
+    }
     a = make_uint4(o[0], o[1], o[2], o[3]);
     b = make_uint4(o[4], o[5], o[6], o[7]);
   }
