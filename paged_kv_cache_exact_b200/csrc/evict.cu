@@ -8,23 +8,26 @@
 //
 // Two kernels:
 //
-// * select_kernel, one CTA per (sequence, kv head).  A thread holds its tokens'
-//   weights in registers as integers of the same order (32768 tokens a CTA;
-//   longer rows are read again).  The threshold is found four bits at a time from
-//   the highest bit in which keys differ: a thread counts its keys into 16
-//   eight-bit counters in registers, then one warp and one block reduction.
-//   (Counting into shared memory puts nearly all keys into a few bins, as weights
-//   crowd near zero, and the atomics serialise; a bit at a time takes a barrier a
-//   bit.)  One scan over all warps' counts gives every kept token its place.  For an 8-bit cache the
-//   CTA also takes every kept row's old scale and gives each destination block the
-//   largest of its rows' scales, before any row moves.
-// * move_kernel, one CTA per (sequence, kv head, K or V, slice of a row):
-//   gathers the kept rows into their new places.  A kept token never moves to a
+// * select_kernel, one CTA per (sequence, kv head).  The weights, as integers of
+//   the same order, pass through shared memory so that a thread holds a run of
+//   consecutive tokens in registers (32768 tokens a CTA; longer rows are read
+//   again, 32768 at a time).  The threshold is found eight bits at a time from the
+//   highest bit in which keys differ: a histogram in shared memory and a scan of
+//   its 256 bins, ending early where a digit's keys are all wanted.  With runs of
+//   tokens a thread's kept ones are consecutive in the result, so one scan over
+//   the threads' counts places them; they are written to shared memory and copied
+//   out whole.  For an 8-bit cache the CTA also takes every kept row's old scale
+//   and gives each destination block the largest of its rows' scales, before any
+//   row moves.
+// * move_kernel, one CTA per (sequence, kv head, K or V, slice of a row), and one
+//   for the weights: gathers the kept rows into their new places.  A kept token never moves to a
 //   higher index, so a CTA that reads a chunk of rows, waits for all its
 //   threads and writes them, chunk by chunk in ascending order, may compact in
 //   place: what it overwrites it has already read, and another CTA never
 //   touches its slice of the rows.  The next chunk's addresses are fetched while
 //   this one's rows are on their way.
+#include <mutex>
+
 #include "cache_attn.cuh"
 #include "q8.cuh"
 
@@ -62,15 +65,26 @@ PKV_DEVINLINE long long token_row(const EvictParams& p, const int32_t* table, in
 // NaN wins over every number.
 PKV_DEVINLINE float max_nan(float a, float b) { return isnan(a) ? a : isnan(b) ? b : fmaxf(a, b); }
 
+// Shared-memory word of a segment's token: a word of padding every 32 keeps the
+// reads of runs of 4, 16 and 32 tokens a thread free of bank conflicts.
+PKV_DEVINLINE int padded(int i) { return i + (i >> 5); }
+
+PKV_DEVINLINE uint32_t warp_scan(uint32_t v, int lane) {           // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
 // kKeys: tokens a thread holds.
 template <int kKeys>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParams p) {
-  __shared__ int part[16][kSelectWarps + 1];                     // every warp's counts of the 16 digits
-  __shared__ int s_digit, s_need;
-  __shared__ uint32_t s_lo[kSelectWarps], s_hi[kSelectWarps];
-  __shared__ uint32_t counts[kKeys * kSelectWarps];              // (equal << 16) | larger, then their prefix sums
-  __shared__ uint32_t row_total[32];
-  static_assert(kSelectWarps == 32 && kKeys <= 32, "one warp sums the warps' counts");
+__global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t words[];               // a segment's keys, then its kept tokens
+  __shared__ __align__(16) int hist[256];
+  __shared__ uint32_t s_lo[kSelectWarps], s_hi[kSelectWarps], s_count[kSelectWarps];
+  __shared__ int s_digit, s_need, s_here;
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int L = clamped_len(p, s);
   if (h == 0 && tid == 0) {
@@ -79,7 +93,6 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   }
   const size_t sh = (size_t)s * p.H_kv + h;
   const float* w = p.weights + sh * p.weights_stride;
-  float* wo = p.weights_out + sh * p.weights_stride;
   int* kept = p.kept + sh * p.budget;
   const int m = min(L, p.budget);
   const int old = m < L ? L - p.recent : 0;         // tokens that compete; none if all stay
@@ -87,30 +100,39 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   constexpr int kSegment = kKeys * kSelectThreads;  // tokens in registers at a time
   const int segments = (L + kSegment - 1) / kSegment;
 
-  uint32_t key[kKeys];                              // of token t0 + i * 1024 + tid
+  uint32_t key[kKeys];                              // of tokens seg * kSegment + tid * kKeys + i
   auto load = [&](int seg) {
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const int t = seg * kSegment + i * kSelectThreads + tid;
-      key[i] = t < L ? order_key(w[t]) : 0u;
+      const int at = i * kSelectThreads + tid;
+      if (seg * kSegment + at < L) words[padded(at)] = order_key(w[seg * kSegment + at]);
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) key[i] = words[padded(tid * kKeys + i)];     // past L: not looked at
+    __syncthreads();
   };
-  load(0);
+  if (segments <= 1) load(0);
 
   // threshold key: fewer than `pick` keys are larger, at least `pick` are larger or equal
   uint32_t threshold = 0xffffffffu;
-  int need = 0;                                     // how many equal to it stay
+  int need = 0;                                     // how many that equal it stay
   if (pick > 0) {
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int seg = 0; seg < segments; ++seg) {
-      if (seg > 0) load(seg);
+    // f(key) for every competing token, one segment from registers, more from memory
+    auto each = [&](auto f) {
+      if (segments <= 1) {
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (seg * kSegment + i * kSelectThreads + tid < old) {
-          lo = min(lo, key[i]);
-          hi = max(hi, key[i]);
-        }
-    }
+        for (int i = 0; i < kKeys; ++i)
+          if (tid * kKeys + i < old) f(key[i]);
+      } else {
+        for (int t = tid; t < old; t += kSelectThreads) f(order_key(w[t]));
+      }
+    };
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    each([&](uint32_t k) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+    });
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi;
@@ -118,74 +140,48 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
     lo = __reduce_min_sync(0xffffffffu, s_lo[lane]);
     hi = __reduce_max_sync(0xffffffffu, s_hi[lane]);
     // The threshold is the `need`-th largest of the keys that agree with `threshold`
-    // above bit `shift`; keys larger than those are counted out of `need` already.
+    // from bit `shift` on; keys larger than those are counted out of `need` already.
     need = pick;
-    const int bits = lo == hi ? 0 : 32 - __clz(lo ^ hi);
-    int shift = (bits + 3) / 4 * 4;
+    int shift = lo == hi ? 0 : 32 - __clz(lo ^ hi);
     threshold = shift == 32 ? 0u : hi >> shift << shift;
     while (shift > 0) {
-      shift -= 4;
-      unsigned long long c0 = 0, c1 = 0;            // counts of digits 0 .. 7 and 8 .. 15, a byte each
-      int count = 0;                                // lane 2d (and 2d + 1): the warp's count of digit d
-      for (int seg = 0; seg < segments; ++seg) {
-        if (segments > 1) load(seg);
-#pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-          const uint32_t d = (key[i] ^ threshold) >> shift;          // threshold has zeros from bit shift + 3 down
-          const unsigned long long one = 1ull << ((d & 7u) * 8u);
-          const bool in = seg * kSegment + i * kSelectThreads + tid < old;
-          if (in && d < 8u) c0 += one;
-          if (in && (d & ~7u) == 8u) c1 += one;
-        }
-        // Over the warp, halving the counts a lane holds with the lanes that share
-        // them (16-bit counts, two a word: 32 keys * 32 lanes fit; REDUX takes
-        // longer than these nine shuffles).
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t two = (uint32_t)((j < 4 ? c0 : c1) >> (16 * (j & 3)));
-          v[j] = (two & 0xffu) | ((two & 0xff00u) << 8);
-        }
-        c0 = c1 = 0;
-#pragma unroll
-        for (int o = 16, n = 4; n >= 1; o >>= 1, n >>= 1) {
-          const bool up = lane & o;
-#pragma unroll
-          for (int j = 0; j < n; ++j) {
-            const uint32_t send = up ? v[j] : v[j + n], keep = up ? v[j + n] : v[j];
-            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
-        }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        // lanes 4j .. 4j + 3 hold digits 2j and 2j + 1
-        count += (lane & 2) ? v[0] >> 16 : v[0] & 0xffffu;
-      }
-      if ((lane & 1) == 0) part[lane >> 1][warp] = count;
+      const int bits = min(shift, 8);
+      shift -= bits;
+      if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      if (warp == 0) {
-        // lane 2d + e sums half the warps' counts of digit d, then the counts of larger digits
-        int n = 0;
+      each([&](uint32_t k) {
+        const uint32_t d = (k ^ threshold) >> shift;                 // threshold has zeros in this digit and below
+        if (d < 256u && (bits == 8 || d < (1u << bits))) atomicAdd(&hist[d], 1);   // an integer sum: any order
+      });
+      __syncthreads();
+      if (warp == 0) {                              // lane l: bins 255 - 8 l and the seven below, from the top
+        const int4 a = *reinterpret_cast<const int4*>(&hist[248 - 8 * lane]);
+        const int4 b = *reinterpret_cast<const int4*>(&hist[252 - 8 * lane]);
+        const int n[8] = {b.w, b.z, b.y, b.x, a.w, a.z, a.y, a.x};
+        int sum = 0;
 #pragma unroll
-        for (int i = 0; i < kSelectWarps / 2; ++i) n += part[lane >> 1][(lane & 1) * (kSelectWarps / 2) + i];
-        n += __shfl_xor_sync(0xffffffffu, n, 1);
-        int from = n;                               // digit d and larger
+        for (int i = 0; i < 8; ++i) sum += n[i];
+        int above = (int)warp_scan((uint32_t)sum, lane) - sum;       // keys in larger bins than this lane's
+        if (above < need && above + sum >= need) {
+          int digit = 255 - 8 * lane, here = 0;
 #pragma unroll
-        for (int o = 2; o < 32; o <<= 1) {
-          const int u = __shfl_down_sync(0xffffffffu, from, o);
-          if (lane + o < 32) from += u;
-        }
-        const uint32_t enough = __ballot_sync(0xffffffffu, from >= need);
-        const int top = 31 - __clz(enough);         // the largest digit with `need` keys from it on (0 has them)
-        if (lane == top) {
-          s_digit = lane >> 1;
-          s_need = need - (from - n);
+          for (int i = 0; i < 8; ++i)
+            if (here == 0) {
+              if (above + n[i] >= need) here = n[i], digit -= i;
+              else above += n[i];
+            }
+          s_digit = digit;
+          s_need = need - above;
+          s_here = here;
         }
       }
       __syncthreads();
-      const int digit = s_digit;
+      threshold |= (uint32_t)s_digit << shift;
       need = s_need;
-      threshold |= (uint32_t)digit << shift;
+      if (s_here == need) {                         // every key from this digit on is wanted: keys with it are
+        need = L;                                   // >= threshold, whose lower bits are zero
+        break;
+      }
     }
   }
 
@@ -193,59 +189,39 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   int base_gt = 0, base_eq = 0;
   for (int seg = 0; seg < segments; ++seg) {
     if (segments > 1) load(seg);
-    const int t0 = seg * kSegment;
-    uint32_t gt_mask = 0, eq_mask = 0;              // bit i: this thread's token i
+    const int t0 = seg * kSegment + tid * kKeys;
+    uint32_t n = 0;                                 // (equal << 16) | larger: a segment has at most 32768 of each
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const int t = t0 + i * kSelectThreads + tid;
-      const bool gt = t < L && (t >= old || (pick > 0 && key[i] > threshold));
-      const bool eq = t < old && pick > 0 && key[i] == threshold;
-      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-      gt_mask |= (uint32_t)gt << i;
-      eq_mask |= (uint32_t)eq << i;
-      if (lane == 0) counts[i * kSelectWarps + warp] = (__popc(be) << 16) | __popc(bg);
+      const int t = t0 + i;
+      const bool gt = t < L && (t >= old || key[i] > threshold);
+      const bool eq = t < old && key[i] == threshold;
+      n += (gt ? 1u : 0u) + (eq ? 0x10000u : 0u);
     }
-    float x[kKeys];                                 // the weights themselves, before any is overwritten
-#pragma unroll
-    for (int i = 0; i < kKeys; ++i)
-      x[i] = ((gt_mask | eq_mask) >> i) & 1u ? w[t0 + i * kSelectThreads + tid] : 0.f;
+    const uint32_t in_warp = warp_scan(n, lane);
+    if (lane == 31) s_count[warp] = in_warp;
     __syncthreads();
-    auto scan = [&](uint32_t v) {                   // inclusive, over the lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-      }
-      return v;
-    };
-    if (warp < kKeys) {                             // warp i: the counts of row i before each warp
-      const uint32_t v = counts[warp * kSelectWarps + lane], sum = scan(v);
-      counts[warp * kSelectWarps + lane] = sum - v;
-      if (lane == 31) row_total[warp] = sum;
-    }
-    __syncthreads();
-    const uint32_t total = lane < kKeys ? row_total[lane] : 0u, row_sum = scan(total);
-    const uint32_t lt = (1u << lane) - 1u;
+    const uint32_t warps = warp_scan(s_count[lane], lane);
+    const uint32_t total = __shfl_sync(0xffffffffu, warps, 31);
+    const uint32_t before = (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0u) + in_warp - n;
+    const int first = base_gt + min(base_eq, need);                 // where this segment's kept tokens start
+    int n_gt = base_gt + (int)(before & 0xffffu), n_eq = base_eq + (int)(before >> 16);
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const bool gt = (gt_mask >> i) & 1u, eq = (eq_mask >> i) & 1u;
-      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-      const uint32_t before = counts[i * kSelectWarps + warp] + __shfl_sync(0xffffffffu, row_sum - total, i);
-      if (!(bg | be)) continue;                     // warp-uniform
-      const int n_gt = base_gt + (int)(before & 0xffff) + __popc(bg & lt);
-      const int n_eq = base_eq + (int)(before >> 16) + __popc(be & lt);
-      if (gt || (eq && n_eq < need)) {
-        const int j = n_gt + min(n_eq, need);
-        kept[j] = t0 + i * kSelectThreads + tid;
-        wo[j] = x[i];                               // j <= t: in place, read already
-      }
+      const int t = t0 + i;
+      const bool gt = t < L && (t >= old || key[i] > threshold);
+      const bool eq = t < old && key[i] == threshold;
+      if (gt || (eq && n_eq < need)) words[n_gt + min(n_eq, need) - first] = t;
+      n_gt += gt;
+      n_eq += eq;
     }
-    const uint32_t all = __shfl_sync(0xffffffffu, row_sum, 31);
-    base_gt += all & 0xffff;
-    base_eq += all >> 16;
+    base_gt += total & 0xffffu;
+    base_eq += total >> 16;
+    __syncthreads();
+    const int last = base_gt + min(base_eq, need);
+    for (int j = first + tid; j < last; j += kSelectThreads) kept[j] = (int)words[j - first];
     __syncthreads();
   }
-  for (int t = m + tid; t < L; t += kSelectThreads) wo[t] = 0.f;
   for (int j = m + tid; j < p.budget; j += kSelectThreads) kept[j] = -1;
   if (!p.k_scales) return;
 
@@ -289,10 +265,40 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictParam
   }
 }
 
+// The weights of one (sequence, head), by the same rule as its rows.
+PKV_DEVINLINE void move_weights(const EvictParams& p) {
+  constexpr int kUnroll = 8;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const int L = clamped_len(p, s), m = min(L, p.budget);
+  const size_t sh = (size_t)s * p.H_kv + h;
+  const int* kept = p.kept + sh * p.budget;
+  const float* w = p.weights + sh * p.weights_stride;
+  float* wo = p.weights_out + sh * p.weights_stride;
+  for (int j0 = 0; j0 < m; j0 += kMoveThreads * kUnroll) {
+    float x[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kMoveThreads + threadIdx.x;
+      x[u] = j < m ? w[kept[j]] : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kMoveThreads + threadIdx.x;
+      if (j < m) wo[j] = x[u];
+    }
+  }
+  for (int t = m + threadIdx.x; t < L; t += kMoveThreads) wo[t] = 0.f;
+}
+
 template <int kCache>
 __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams p) {
   constexpr int kMoveUnroll = move_unroll<kCache>();
   const int slices = p.row_bytes / p.slice_bytes;
+  if ((int)blockIdx.x == 2 * slices) {
+    move_weights(p);
+    return;
+  }
   const bool is_v = (int)blockIdx.x >= slices;
   const int slice = blockIdx.x - (is_v ? slices : 0);
   const int h = blockIdx.y, s = blockIdx.z;
@@ -359,22 +365,43 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams
   }
 }
 
+template <int kKeys>
+cudaError_t launch_select(const EvictParams& p, dim3 grid, cudaStream_t stream) {
+  // The shared-memory limit is an attribute per device; host threads may get
+  // here at once, so the once-per-device record is kept under a lock.
+  constexpr int kSmem = (kKeys * kSelectThreads + kKeys * kSelectWarps) * 4;
+  static bool done[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      e = cudaFuncSetAttribute(select_kernel<kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  select_kernel<kKeys><<<grid, kSelectThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   const dim3 rows(p.H_kv, p.num_seqs);
   // registers for the longest sequence's weights: 4, 16 or 32 a thread
-  if (p.max_seq_len <= 4 * kSelectThreads) select_kernel<4><<<rows, kSelectThreads, 0, stream>>>(p);
-  else if (p.max_seq_len <= 16 * kSelectThreads) select_kernel<16><<<rows, kSelectThreads, 0, stream>>>(p);
-  else select_kernel<32><<<rows, kSelectThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = p.max_seq_len <= 4 * kSelectThreads    ? launch_select<4>(p, rows, stream)
+                  : p.max_seq_len <= 16 * kSelectThreads ? launch_select<16>(p, rows, stream)
+                                                         : launch_select<32>(p, rows, stream);
   if (e != cudaSuccess) return e;
   // Wide slices make whole 128-byte requests; narrow ones make more CTAs of few
   // (sequence, head) pairs.  Halve while there are fewer than 4 CTAs per SM.
   EvictParams q = p;
   q.slice_bytes = p.row_bytes < 128 ? p.row_bytes : 128;
   while (q.slice_bytes > 32 && 2LL * p.row_bytes / q.slice_bytes * p.H_kv * p.num_seqs < 148LL * 4) q.slice_bytes /= 2;
-  const dim3 grid(2 * p.row_bytes / q.slice_bytes, p.H_kv, p.num_seqs);
+  const dim3 grid(2 * p.row_bytes / q.slice_bytes + 1, p.H_kv, p.num_seqs);      // + the weights
   if (p.cache_dtype == PKV_I8) move_kernel<PKV_I8><<<grid, kMoveThreads, 0, stream>>>(q);
   else if (p.cache_dtype == PKV_E4M3) move_kernel<PKV_E4M3><<<grid, kMoveThreads, 0, stream>>>(q);
   else move_kernel<PKV_BF16><<<grid, kMoveThreads, 0, stream>>>(q);
