@@ -18,72 +18,77 @@ template <int kCache> PKV_DEVINLINE constexpr float code_max() {
   return kCache == PKV_I8 ? 127.f : 448.f;
 }
 
-// Nearest e4m3 code (RNE, saturating).
-PKV_DEVINLINE uint32_t f32_to_e4m3(float x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f32 c, %1, %2;\n\tcvt.u32.u16 %0, c;\n\t}"
-      : "=r"(r) : "f"(0.f), "f"(x));
-  return r & 0xffu;
+// Exact rounding of a quotient num / den to a code.  An approximate quotient q
+// (relative error <= 2^-22) finds the tie h nearest to it, the point half way
+// between two neighbouring codes, and the sign of num - h * den says on which side
+// of h the quotient lies:
+//
+// * ties are common, not rare: a scale is amax / qmax with amax a bf16 number, so
+//   quotients of bf16 elements are ratios of small integers;
+// * h has at most 9 significant bits, so near a tie num - h * den is exact in one
+//   fused multiply-add (and one more term where num itself is the product of a
+//   code and its old scale), and elsewhere its sign is not in doubt.
+//
+// h, moved a little to the quotient's side, is then rounded to nearest even.
+// `residual(i, h)` has the sign of num_i - h * den.
+template <int kCache, typename Residual>
+PKV_DEVINLINE float settle_half(float q, int i, Residual residual) {
+  // int8, or e4m3's subnormal codes in units of 2^-9: ties are halves
+  const float unit = kCache == PKV_I8 ? 1.f : 0.001953125f;
+  const float v = kCache == PKV_I8 ? q : q * 512.f;
+  const float n = (v + 12582912.f) - 12582912.f;                     // nearest integer
+  const float half = n + copysignf(0.5f, v - n);
+  const float r = residual(i, half * unit);
+  return (half + (r == 0.f ? 0.f : copysignf(0.0009765625f, r))) * unit;
 }
 
-// The code nearest to the real quotient num / den, ties to even.  `num` is a
-// product that float64 holds exactly (a row's element, or a code times its
-// old scale) and den a float32 number, so num / den differs from a tie by at
-// least 2^-35 of itself or not at all: one float64 division decides.
-template <int kCache>
-__device__ __noinline__ uint32_t code_exact(double num, double den) {
-  const double y = num / den;
-  if (kCache == PKV_I8) {
-    const double n = fmin(fmax(rint(y), -127.0), 127.0);
-    return static_cast<uint32_t>(static_cast<int>(n)) & 0xffu;
-  }
-  // to float32 by round-to-odd, after which the rounding to e4m3 is the only one
-  float f = __double2float_rz(y);
-  if (static_cast<double>(f) != y) f = __uint_as_float(__float_as_uint(f) | 1u);
-  return f32_to_e4m3(f);
-}
-
-// Four codes (a word) from approximate quotients q (relative error <= 2^-22): q
-// decides unless it lies next to a tie (or, for e4m3, in the subnormal range),
-// where all four ask `exact(i)`.  That is about one element in 10^5 for int8 and
-// one in 10^4 for e4m3, so the float64 division costs nothing on average.  int8
-// rounds by adding 1.5 * 2^23, which leaves the integer in the low mantissa bits:
-// conversion instructions run at a quarter of the rate.
-template <int kCache, typename Exact>
-PKV_DEVINLINE uint32_t codes_of4(const float (&q)[4], Exact exact) {
-  bool near_tie;
+// Four codes (a word) from approximate quotients.
+template <int kCache, typename Residual>
+PKV_DEVINLINE uint32_t codes_of4(float (&q)[4], Residual residual) {
   uint32_t word;
   if (kCache == PKV_I8) {
-    float y[4], off = 1.f;
+    // Few blocks have ties (127 is a prime): look for them first.  Rounding adds
+    // 1.5 * 2^23, which leaves the integer in the low mantissa bits: conversion
+    // instructions run at a quarter of the rate.
+    float off = 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = q[i] + 12582912.f;
-      off = fminf(off, fabsf(fabsf(q[i] - (y[i] - 12582912.f)) - 0.5f));
+    for (int i = 0; i < 4; ++i)
+      off = fminf(off, fabsf(fabsf(q[i] - ((q[i] + 12582912.f) - 12582912.f)) - 0.5f));
+    if (off < 4e-5f) {                                               // 127 * 2^-22 = 3.03e-5
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = settle_half<kCache>(q[i], i, residual);
     }
-    near_tie = off < 1e-4f;
-    word = __byte_perm(__byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040),
-                       __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040), 0x5410);
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __float_as_uint(q[i] + 12582912.f);
+    word = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
   } else {
-    uint32_t tie = 0xffffffffu, small = 0xffffffffu;
+    // A tie has 0x80000 in the 20 mantissa bits that are dropped: the one in q's
+    // own cell decides every element, so there is nothing to look for.
+    float x[4], least = fabsf(q[0]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = __float_as_uint(q[i]);
-      tie = min(tie, (b + 8u - 0x80000u) & 0xfffffu);                // 20 bits are dropped: a tie has 0x80000 there
-      small = min(small, (b & 0x7fffffffu) - 1u);                    // zero is no trouble
+      const float h = __uint_as_float((__float_as_uint(q[i]) & 0xfff00000u) | 0x80000u);
+      const float r = residual(i, h);
+      x[i] = h + (r == 0.f ? 0.f : copysignf(h * 9.5367432e-7f, r));
+      least = fminf(least, fabsf(q[i]));
     }
-    near_tie = tie <= 16u || small < 0x3c800000u - 1u;               // 2^-6
+    if (least < 0.015625f) {                                         // below 2^-6 codes are 2^-9 apart
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (fabsf(q[i]) < 0.015625f) x[i] = settle_half<kCache>(q[i], i, residual);
+    }
     asm("{\n\t.reg .b16 a, b;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
         "mov.b32 %0, {a, b};\n\t}"
-        : "=r"(word) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
-  }
-  if (near_tie) {
-    word = 0;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) word |= exact(i) << (8 * i);
+        : "=r"(word) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
   }
   return word;
 }
+
+// Scales below 2^-64 (and what they divide) are multiplied by 2^64 first, so that
+// no residual is a subnormal number.
+constexpr float kTinyScale = 5.42101086e-20f, kTinyLift = 1.8446744e19f;   // 2^-64, 2^64
 
 // The four values of a word of codes as float32 (exact).
 template <int kCache>
@@ -108,13 +113,15 @@ PKV_DEVINLINE void values_of4(uint32_t w, float (&x)[4]) {
 // ratio = s_old / s_new rounded to float32.
 template <int kCache>
 PKV_DEVINLINE uint32_t requantize4(uint32_t w, float ratio, float s_old, float s_new) {
+  const float lift = s_new < kTinyScale ? kTinyLift : 1.f;
+  const float a = s_old * lift, b = s_new * lift;
   float c[4], q[4];
   values_of4<kCache>(w, c);
 #pragma unroll
   for (int i = 0; i < 4; ++i) q[i] = c[i] * ratio;
-  return codes_of4<kCache>(q, [&](int i) {
-    const float v = i == 0 ? c[0] : i == 1 ? c[1] : i == 2 ? c[2] : c[3];
-    return code_exact<kCache>(static_cast<double>(v) * static_cast<double>(s_old), static_cast<double>(s_new));
+  return codes_of4<kCache>(q, [&](int i, float h) {
+    const float v = c[i], p = v * a;
+    return fmaf(-h, b, p) + fmaf(v, a, -p);                          // p is rounded; its error is exact
   });
 }
 

@@ -165,15 +165,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_ke
       for (int r = part; r < off; r += parts)
         code[r * code_stride] = requantize4<kCache>(code[r * code_stride], ratio, old, s);
     }
-    const float inv = __fdiv_rn(1.f, s);
+    const float lift = s < kTinyScale ? kTinyLift : 1.f;
+    const float den = s * lift, inv = __fdiv_rn(1.f, den);
     auto store = [&](int r, const Row4<T>& y) {
-      float q[4];
+      float v[4], q[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = y.at(i) * inv;
-      const uint32_t w = codes_of4<kCache>(q, [&](int i) {
-        const float v = i == 0 ? y.at(0) : i == 1 ? y.at(1) : i == 2 ? y.at(2) : y.at(3);
-        return code_exact<kCache>(static_cast<double>(v), static_cast<double>(s));
-      });
+      for (int i = 0; i < 4; ++i) {
+        v[i] = y.at(i) * lift;
+        q[i] = v[i] * inv;
+      }
+      const uint32_t w = codes_of4<kCache>(q, [&](int i, float h) { return fmaf(-h, den, v[i]); });
       code[(size_t)(off + r) * code_stride] = broken ? 0u : w;
     };
 #pragma unroll
