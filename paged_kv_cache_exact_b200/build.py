@@ -35,12 +35,16 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
 REG_GUARDS = {"prefill_sm100.cu": ("prefill_kernel", "kLaunchRegs")}
 
 
-def check_launch_registers(src_name: str, ptxas_log: str) -> None:
+# The same file's kernel for 8-bit caches, which has four warpgroups.
+CODES_GUARD = ("attend_codes_kernel", "kLaunchRegsQ8")
+
+
+def check_launch_registers(src_name: str, ptxas_log: str, guard=None) -> None:
     """Fail the build unless every guarded kernel compiled to exactly the
     register count its source declares: a different count would make the
     kernel's register split wait forever (more registers requested than the
     launch holds) or waste registers."""
-    kernel, const = REG_GUARDS[src_name]
+    kernel, const = guard or REG_GUARDS[src_name]
     with open(os.path.join(CSRC, src_name)) as f:
         m = re.search(r"constexpr\s+int\s+" + const + r"\s*=\s*(\d+)\s*;", f.read())
     if not m:
@@ -102,6 +106,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
             if src in REG_GUARDS:
                 try:
                     check_launch_registers(src, r.stdout + r.stderr)
+                    check_launch_registers(src, r.stdout + r.stderr, CODES_GUARD)
                 except RuntimeError:
                     os.remove(cmd[-1])        # never link an object that failed the check
                     raise

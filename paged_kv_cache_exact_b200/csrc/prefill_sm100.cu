@@ -46,17 +46,19 @@
 //   softmax (as the decode kernel does) and its V rows are zeroed, and
 //   PKV_DEVERR_BAD_PAGE is recorded.
 //
-// 8-bit caches (kCache = PKV_I8 or PKV_E4M3, paged).  int8 and e4m3 codes are
-// exact in bf16, so the MMAs run on bf16 codes and the scales are applied in
-// float32: a key block's scale joins the softmax scale, a value block's scale
-// multiplies P before it is rounded to bf16.  Warps 10 and 11 take the place of
-// the TMA loads: each streams its 64 rows of a K or V tile in pieces of 16 rows
-// (a piece lies in one page and one scale block) through a ring of cp.async
-// stages, converts the codes in registers and writes the swizzled bf16 tile that
-// TMA would have written.  A lane converts exactly the bytes it copied, so a
-// piece needs no barrier, and the ring keeps kPieces pieces per warp in flight.
-// Warp 10 also does the loader's other work (Q loads, item claims); rows past
-// the sequence and rows of bad pages are written as zeros.
+// 8-bit caches (kCache = PKV_I8 or PKV_E4M3, paged; attend_codes_kernel).  int8
+// and e4m3 codes are exact in bf16, so the MMAs run on bf16 codes and the scales
+// are applied in float32: a key block's scale joins the softmax scale, a value
+// block's scale multiplies P before it is rounded to bf16.  A fourth warpgroup
+// joins and warps 10-15 take the place of the TMA loads: the tiles' 16-row pieces
+// (a piece lies in one page and one scale block) go round the six warps, each of
+// which copies its next pieces with cp.async, converts the codes in registers and
+// writes the swizzled bf16 tile that TMA would have written.  A lane converts
+// exactly the bytes it copied, so a piece needs no barrier.  Warp 10 also does the
+// loader's other work (Q loads, item claims); rows past the sequence and rows of
+// bad pages are written as zeros.  Two converting warps (in the two idle ones) took
+// 10500 cycles a tile, as one warp issues a dependent instruction every four
+// cycles or so; what the MMAs and the softmax need is 3400.
 #include <cuda.h>
 
 #include <mutex>
@@ -129,11 +131,20 @@ constexpr int kSmemBytes = kSmemUsed + 1024;       // slack for 1024-byte alignm
 // 8-bit caches: scales of the K/V tiles in flight, then each converter warp's
 // ring of 2 KB pieces (16 rows of 128 codes).
 constexpr int kScaleSlots = 8;
-constexpr int kPieces = 6;
+constexpr int kConverters = 6;                                     // warps 10 .. 15
+constexpr int kPieces = 2;                                         // of a warp's pieces in its ring
 constexpr int kPieceBytes = 16 * D;
 constexpr int kOffScale = (kSmemUsed + 15) & ~15;                  // float[kScaleSlots][16]: 8 ks, 8 vs
 constexpr int kOffPiece = kOffScale + kScaleSlots * 64;
-constexpr int kSmemBytesQ8 = kOffPiece + 2 * kPieces * kPieceBytes + 1024;
+constexpr int kSmemBytesQ8 = kOffPiece + kConverters * kPieces * kPieceBytes + 1024;
+// Four warpgroups: launched at 128 registers, 200 for the softmax warpgroups and 56
+// for the other two.
+constexpr int kThreadsQ8 = 512;
+constexpr int kLaunchRegsQ8 = 128;
+constexpr int kRegsSoftmaxQ8 = 200;
+constexpr int kRegsSideQ8 = 56;
+static_assert(2 * 128 * kRegsSoftmaxQ8 + 2 * 128 * kRegsSideQ8 <= kThreadsQ8 * kLaunchRegsQ8,
+              "register split exceeds the launch allocation");
 static_assert(kSmemBytesQ8 <= 227 * 1024, "shared memory");
 
 // TMEM columns.
@@ -236,9 +247,8 @@ PKV_DEVINLINE void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
 // kCache: PKV_BF16, or the code type of an 8-bit paged cache.  kLse: every row's
 // log2 of its softmax sum goes to p.lse (+infinity for a row that sees no key).
 template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
-__global__ void __launch_bounds__(kThreads, 1)
-prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+__device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                             const PrefillParams& p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -257,10 +267,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t cnt = 1;
       if (i >= kBarPHalf && i < kBarPFull + kQTiles) cnt = 128;   // one arrival per softmax thread
-      if (i >= kBarItemFree && i < kBarItemFree + 2) cnt = kItemReaders + kQ8;   // + the second converter
-      // one arrival per converting thread
+      if (i >= kBarItemFree && i < kBarItemFree + 2) cnt = kItemReaders + (kQ8 ? kConverters - 1 : 0);
+      // one arrival per lane and piece
       if (kQ8 && ((i >= kBarKFull && i < kBarKFull + kStages) || (i >= kBarVFull && i < kBarVFull + kStages)))
-        cnt = 64;
+        cnt = BN / 16 * 32;
       mbar_init(bar(i), cnt);
     }
     for (int s = 0; s < kMaskSlots; ++s) mask_slot[s] = mask_word(s - kMaskSlots, 0);
@@ -307,16 +317,24 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     return v;
   };
 
-  if (warp >= 8) regs_decrease<kRegsSide>();
+  if (warp >= 8) regs_decrease<kQ8 ? kRegsSideQ8 : kRegsSide>();
 
-  if (kQ8 && (warp == 10 || warp == 11)) {
+  if (kQ8 && warp >= 10) {
     // ------------------------------------------- loader and converters, 8-bit --
-    const int half = warp - 10;                      // rows 64 half .. 64 half + 63 of every tile
-    const bool lead = half == 0;                     // loads Q and claims items
-    const uint32_t ring = sbase + kOffPiece + half * kPieces * kPieceBytes + lane * 16;
+    const int part = warp - 10;                      // takes pieces part, part + kConverters, ...
+    const bool lead = part == 0;                     // loads Q and claims items
+    const uint32_t ring = sbase + kOffPiece + part * kPieces * kPieceBytes + lane * 16;
+    const uint8_t* raw0 = smem + kOffPiece + part * kPieces * kPieceBytes + lane * 16;
     float* scales = reinterpret_cast<float*>(smem + kOffScale);
     const int ck = lane & 7, rk = lane >> 3;         // this lane's 16-byte chunk, and row + 4 u
-    const size_t stride = (size_t)p.H_kv * D;
+    const int stride = p.H_kv * D;
+    // where this lane's codes go in a tile: chunks 2c, 2c + 1 of a row's 64-column
+    // block, by the row's swizzle.  The lanes of the second block store them the
+    // other way round, so that eight lanes meet eight bank groups.
+    const bool swap = ck >= 4;
+    const int col = (ck >> 2) * kHalfBytes + rk * 128;
+    const int at0 = ((2 * (ck & 3) + swap) ^ rk) << 4;              // rows rk, rk + 8; rows rk + 4, + 12: ^ 64
+    const int at1 = ((2 * (ck & 3) + !swap) ^ rk) << 4;
     int kv_it = 0, claims = 0;
     int q_it[kQTiles] = {0, 0};
     uint32_t q_pend = 0;                             // Q tile t: bit t loads pending, bit 2 + t their parity
@@ -349,17 +367,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         q_pend = (q_pend & ~(5u << t)) | (1u << t) | ((uint32_t)(q_it[t] & 1) << (2 + t));
         return true;
       };
-      const uint8_t* kb = static_cast<const uint8_t*>(p.K) + (size_t)g.kvh * D + ck * 16;
-      const uint8_t* vb = static_cast<const uint8_t*>(p.V) + (size_t)g.kvh * D + ck * 16;
+      const size_t lane_off = (size_t)g.kvh * D + ck * 16 + (size_t)rk * stride;
+      const uint8_t* kb = static_cast<const uint8_t*>(p.K) + lane_off;
+      const uint8_t* vb = static_cast<const uint8_t*>(p.V) + lane_off;
       const int32_t* trow = p.block_table + (size_t)g.b * p.max_pages;
       const int n_pages = (g.kv_len + p.page_size - 1) >> p.page_shift;
-      // Pieces of this warp: tile j has 4 of K, then 4 of V.
-      const int total = nmax * 8;
+      // Pieces: tile j has 8 of K, then 8 of V.
+      const int total = nmax * 16;
       int held = -32, entry = -1;                    // lane l holds the table entry of page held + l
-      auto fetch = [&](int q) {                      // start piece q's copy (always commits a group)
+      auto fetch = [&](int q, int slot) {            // start piece q's copy (always commits a group)
         if (q < total) {
-          const int j = q >> 3;
-          const int r0 = 64 * half + 16 * (q & 3);   // first row in the tile
+          const int j = q >> 4;
+          const int r0 = 16 * (q & 7);               // first row in the tile
           const int tok = j * BN + r0;
           const int page = tok >> p.page_shift;
           if (page < held || page >= held + 32) {    // warp-uniform
@@ -370,66 +389,54 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const bool live = tok < g.kv_len;
           const bool good = live && phys >= 0 && phys < p.num_pages;
           const size_t row = good ? (((size_t)phys << p.page_shift) + (tok & (p.page_size - 1))) : 0;
-          const uint8_t* src = (q & 4) ? vb : kb;
-          const uint32_t dst = ring + (q % kPieces) * kPieceBytes;
+          const uint8_t* src = ((q & 8) ? vb : kb) + row * stride;
+          const int left = good ? g.kv_len - tok - rk : 0;             // this lane's rows: 4 u < left
+          const uint32_t dst = ring + slot * kPieceBytes;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            cp_async16(dst + u * 512, src + (row + rk + 4 * u) * stride,
-                       good && tok + rk + 4 * u < g.kv_len);
-          if (!(q & 4) && lane < 2) {                // with K: both scales of the piece
-            float* slot = scales + ((kv_it + j) % kScaleSlots) * 16 + lane * 8 + (r0 >> 4);
+          for (int u = 0; u < 4; ++u) cp_async16(dst + u * 512, src + 4 * u * stride, 4 * u < left);
+          if (!(q & 8) && lane < 2) {                // with K: both scales of the piece
+            float* at = scales + ((kv_it + j) % kScaleSlots) * 16 + lane * 8 + (q & 7);
             if (good) {
               const float* from = (lane ? p.v_scales : p.k_scales) + (row >> p.block_shift) * p.H_kv + g.kvh;
-              cp_async4(smem_u32(slot), from);
+              cp_async4(smem_u32(at), from);
             } else {
-              *slot = live && lane == 0 ? -1.f : 1.f;    // a negative key scale: keys of a bad page
+              *at = live && lane == 0 ? -1.f : 1.f;  // a negative key scale: keys of a bad page
             }
             if (live && !good && lane == 0) flag_error(p.err, PKV_DEVERR_BAD_PAGE);
           }
         }
         cp_async_commit();
       };
-#pragma unroll 1
-      for (int q = 0; q < kPieces; ++q) fetch(q);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) fetch(part + i * kConverters, i);
       if (lead && g.n[0] > 0) ok = load_q(0);
       if (ok && lead && g.n[1] > 0) ok = load_q(1);
+      int slot = 0;
 #pragma unroll 1
-      for (int q = 0; q < total && ok; ++q) {
-        const int it = kv_it + (q >> 3);
+      for (int q = part; q < total && ok; q += kConverters) {
+        const int it = kv_it + (q >> 4);
         const int st = it % kStages;
-        const bool is_v = q & 4;
-        if ((q & 3) == 0) {
-          if (lead && !claimed && claim_live && (q >> 3) >= nmax - kClaimLead) claim();
-          ok = wwait((is_v ? kBarVEmpty : kBarKEmpty) + st, ((it / kStages) & 1) ^ 1);
-          if (!ok) break;
-        }
+        const bool is_v = q & 8;
+        if (lead && !claimed && claim_live && (q >> 4) >= nmax - kClaimLead) claim();
+        ok = wwait((is_v ? kBarVEmpty : kBarKEmpty) + st, ((it / kStages) & 1) ^ 1);
+        if (!ok) break;
         cp_async_wait<kPieces - 1>();
-        const uint8_t* raw = smem + kOffPiece + half * kPieces * kPieceBytes + (q % kPieces) * kPieceBytes + lane * 16;
-        uint4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const uint4*>(raw + u * 512);
-        uint8_t* tile = smem + (is_v ? kOffV : kOffK) + st * kTileBytes + (ck >> 2) * kHalfBytes;
+        uint8_t* tile = smem + (is_v ? kOffV : kOffK) + st * kTileBytes + (q & 7) * 16 * 128 + col;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = 64 * half + 16 * (q & 3) + rk + 4 * u;
+          const uint4 x = *reinterpret_cast<const uint4*>(raw0 + slot * kPieceBytes + u * 512);
           uint4 a, b;
-          codes_to_bf16<kCache>(x[u].x, a.x, a.y);
-          codes_to_bf16<kCache>(x[u].y, a.z, a.w);
-          codes_to_bf16<kCache>(x[u].z, b.x, b.y);
-          codes_to_bf16<kCache>(x[u].w, b.z, b.w);
-          // chunks 2c, 2c + 1 of the row's 64-column block; the lanes of the second
-          // block store them the other way round, so that 8 lanes meet 8 banks' groups
-          const int c0 = 2 * (ck & 3);
-          const bool swap = ck >= 4;
-          uint8_t* at = tile + r * 128;
-          *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? b : a;
-          *reinterpret_cast<uint4*>(at + (((c0 + !swap) ^ (r & 7)) << 4)) = swap ? a : b;
+          codes_to_bf16<kCache>(x.x, a.x, a.y);
+          codes_to_bf16<kCache>(x.y, a.z, a.w);
+          codes_to_bf16<kCache>(x.z, b.x, b.y);
+          codes_to_bf16<kCache>(x.w, b.z, b.w);
+          *reinterpret_cast<uint4*>(tile + u * 512 + (at0 ^ ((u & 1) << 6))) = swap ? b : a;
+          *reinterpret_cast<uint4*>(tile + u * 512 + (at1 ^ ((u & 1) << 6))) = swap ? a : b;
         }
-        if ((q & 3) == 3) {
-          fence_proxy_async_smem();
-          mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
-        }
-        fetch(q + kPieces);
+        fence_proxy_async_smem();
+        mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
+        fetch(q + kPieces * kConverters, slot);
+        slot = slot == kPieces - 1 ? 0 : slot + 1;
       }
       if (!ok) break;
       cp_async_wait<0>();
@@ -790,7 +797,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------- softmax --
-    regs_increase<kRegsSoftmax>();
+    regs_increase<kQ8 ? kRegsSoftmaxQ8 : kRegsSoftmax>();
     const int t = warp >> 2;                         // Q tile of this warpgroup
     const int r = threadIdx.x & 127;                 // row in tile = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -1032,6 +1039,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   }
 }
 
+template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
+  prefill_body<kPaged, kFp8QK, kCache, kLse>(tmQ, tmK, tmV, p);
+}
+
+template <int kCache, bool kLse>
+__global__ void __launch_bounds__(kThreadsQ8, 1)
+attend_codes_kernel(const __grid_constant__ CUtensorMap tmQ, const PrefillParams p) {
+  prefill_body<true, false, kCache, kLse>(tmQ, tmQ, tmQ, p);       // only Q is loaded by TMA
+}
+
 // ----------------------------------------------------------------- host side --
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -1071,36 +1091,42 @@ bool encode_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint6
 }
 
 // Dynamic shared memory is a per-device function attribute; host threads may
-// launch concurrently, so the once-per-device record is kept under a lock.
-template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
-cudaError_t set_smem_attr() {
-  static bool done[64] = {};
+// launch concurrently, so the once-per-device record (one per kernel) is kept
+// under a lock.  The in-kernel register split assumes the exact launch allocation
+// `regs` (the build checks it too).
+template <typename Kernel>
+cudaError_t prepare_kernel(Kernel kernel, int regs, int smem, bool (&done)[64]) {
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::lock_guard<std::mutex> lock(mu);
   if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-  // The in-kernel register split assumes this exact launch allocation (the
-  // build checks it too).
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, prefill_kernel<kPaged, kFp8QK, kCache, kLse>);
+  e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-  e = cudaFuncSetAttribute(prefill_kernel<kPaged, kFp8QK, kCache, kLse>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kCache != PKV_BF16 ? kSmemBytesQ8 : kSmemBytes);
+  if (fa.numRegs != regs) return cudaErrorNotSupported;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
 }
 
-template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
+template <bool kPaged, bool kFp8QK, bool kLse>
 cudaError_t launch_variant(dim3 grid, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const PrefillParams& p, cudaStream_t stream) {
-  const cudaError_t e = set_smem_attr<kPaged, kFp8QK, kCache, kLse>();
+  static bool done[64] = {};
+  const cudaError_t e = prepare_kernel(prefill_kernel<kPaged, kFp8QK, PKV_BF16, kLse>, kLaunchRegs, kSmemBytes, done);
   if (e != cudaSuccess) return e;
-  prefill_kernel<kPaged, kFp8QK, kCache, kLse>
-      <<<grid, kThreads, kCache != PKV_BF16 ? kSmemBytesQ8 : kSmemBytes, stream>>>(tq, tk, tv, p);
+  prefill_kernel<kPaged, kFp8QK, PKV_BF16, kLse><<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <int kCache, bool kLse>
+cudaError_t launch_codes(dim3 grid, const CUtensorMap& tq, const PrefillParams& p, cudaStream_t stream) {
+  static bool done[64] = {};
+  const cudaError_t e = prepare_kernel(attend_codes_kernel<kCache, kLse>, kLaunchRegsQ8, kSmemBytesQ8, done);
+  if (e != cudaSuccess) return e;
+  attend_codes_kernel<kCache, kLse><<<grid, kThreadsQ8, kSmemBytesQ8, stream>>>(tq, p);
   return cudaGetLastError();
 }
 
@@ -1119,7 +1145,7 @@ cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t stream) {
   if (!encode_3d(&tq, p.Q, D, p.q_len, (uint64_t)p.B * p.H, qk_row, qk_row * p.q_len, BM, 1, f8))
     return cudaErrorInvalidValue;
   if (q8) {
-    tk = tv = tq;                                    // not read: the codes are not loaded by TMA
+    // the codes are not loaded by TMA
   } else if (p.paged) {
     // pages [P, ps, H_kv, d] viewed as [P*ps tokens, H_kv, d]; one box = one page's rows.
     const uint32_t rows = p.page_size < BN ? p.page_size : BN;
@@ -1151,16 +1177,15 @@ cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t stream) {
     q.head_group = (int)hg;
   }
   if (p.cache_dtype == PKV_I8)
-    return p.lse ? launch_variant<true, false, PKV_I8, true>(grid, tq, tk, tv, q, stream)
-                 : launch_variant<true, false, PKV_I8, false>(grid, tq, tk, tv, q, stream);
+    return p.lse ? launch_codes<PKV_I8, true>(grid, tq, q, stream) : launch_codes<PKV_I8, false>(grid, tq, q, stream);
   if (p.cache_dtype == PKV_E4M3)
-    return p.lse ? launch_variant<true, false, PKV_E4M3, true>(grid, tq, tk, tv, q, stream)
-                 : launch_variant<true, false, PKV_E4M3, false>(grid, tq, tk, tv, q, stream);
+    return p.lse ? launch_codes<PKV_E4M3, true>(grid, tq, q, stream)
+                 : launch_codes<PKV_E4M3, false>(grid, tq, q, stream);
   if (p.paged)
-    return p.lse ? launch_variant<true, false, PKV_BF16, true>(grid, tq, tk, tv, q, stream)
-                 : launch_variant<true, false, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
-  if (f8) return launch_variant<false, true, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
-  return launch_variant<false, false, PKV_BF16, false>(grid, tq, tk, tv, q, stream);
+    return p.lse ? launch_variant<true, false, true>(grid, tq, tk, tv, q, stream)
+                 : launch_variant<true, false, false>(grid, tq, tk, tv, q, stream);
+  if (f8) return launch_variant<false, true, false>(grid, tq, tk, tv, q, stream);
+  return launch_variant<false, false, false>(grid, tq, tk, tv, q, stream);
 }
 
 }  // namespace pkv
