@@ -90,7 +90,7 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
   p.ws_o = static_cast<float*>(take(w.o));
   p.ws_ml = static_cast<float2*>(take(w.ml));
   p.logits = static_cast<float*>(take(w.logits));
-  p.lse = static_cast<float*>(take(w.lse));
+  p.neg_lse = static_cast<float*>(take(w.lse));
   p.num_seqs = num_seqs, p.q_len = q_len, p.H = H, p.H_kv = H_kv;
   p.page_size = page_size, p.page_shift = log2i(page_size), p.block_shift = q8 ? log2i(block_tokens) : 0;
   p.num_pages = num_pages, p.max_pages = max_pages_per_seq, p.max_seq_len = max_seq_len;
@@ -112,7 +112,7 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
   f.causal = causal, f.scale_log2 = p.scale_log2;
   if (q8) f.cache_dtype = cache_dtype, f.block_shift = p.block_shift, f.k_scales = p.k_scales, f.v_scales = p.v_scales;
   p.lse_stride = (int)lse_rows(q_len);
-  f.lse = p.lse, f.lse_stride = p.lse_stride;
+  f.neg_lse = p.neg_lse, f.lse_stride = p.lse_stride;
   const cudaError_t e = pkv::launch_prefill_bf16(f, st);
   if (e != cudaSuccess || !weights) return pkv::cuda_status(e);
   return pkv::cuda_status(pkv::launch_prompt_weights(p, st));

@@ -46,7 +46,7 @@ struct CacheAttnParams {
   float* ws_o;                 // [S, H, max_splits, d]
   float2* ws_ml;               // [S, H, max_splits]: max in log2 units, sum
   float* logits;               // [S, H_kv, logit_tokens, H / H_kv]: scores in log2 units
-  float* lse;                  // [S, H, lse_stride]: log2 of each row's sum, +infinity past q_len
+  float* neg_lse;              // [S, H, lse_stride]: minus log2 of each row's sum, -infinity past q_len
   unsigned int* err;
   int num_seqs, q_len, H, H_kv, page_size, page_shift, block_shift, num_pages, max_pages, max_seq_len;
   int split_tokens, max_splits, weights_stride, logit_tokens, lse_stride;

@@ -102,9 +102,9 @@ struct PrefillParams {
   int block_shift;             // log2 of the tokens a scale covers
   const float* k_scales;       // [P, ps / block, H_kv]
   const float* v_scales;
-  // Row sums for the attention weights (null: not wanted): log2 of every row's
-  // sum, [B, H, lse_stride], lse_stride >= q_len.
-  float* lse;
+  // Row sums for the attention weights (null: not wanted): minus log2 of every
+  // row's sum, [B, H, lse_stride], lse_stride >= q_len.
+  float* neg_lse;
   int lse_stride;
 };
 

@@ -244,8 +244,9 @@ PKV_DEVINLINE void codes_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 // ----------------------------------------------------------------------------
-// kCache: PKV_BF16, or the code type of an 8-bit paged cache.  kLse: every row's
-// log2 of its softmax sum goes to p.lse (+infinity for a row that sees no key).
+// kCache: PKV_BF16, or the code type of an 8-bit paged cache.  kLse: minus every
+// row's log2 of its softmax sum goes to p.neg_lse (-infinity for a row that sees no
+// key: as the exponent's offset it makes every weight of the row 0).
 template <bool kPaged, bool kFp8QK, int kCache, bool kLse>
 __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                              const PrefillParams& p) {
@@ -997,9 +998,9 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUten
         tc_fence_after();
       }
       const bool store = row < p.q_len;
-      if (kLse && row < p.lse_stride)                // rows past q_len (tile padding): +infinity
-        p.lse[((size_t)g.b * p.H + g.h) * p.lse_stride + row] =
-            store && n > 0 && l != 0.f ? m_ref + log2f(l) : INFINITY;
+      if (kLse && row < p.lse_stride)                // rows past q_len (tile padding): -infinity
+        p.neg_lse[((size_t)g.b * p.H + g.h) * p.lse_stride + row] =
+            store && n > 0 && l != 0.f ? -(m_ref + log2f(l)) : -INFINITY;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.O) +
                            (((size_t)g.b * p.H + g.h) * p.q_len + (store ? row : 0)) * D;
       const float inv = (n > 0 && l > 0.f) ? 1.f / l : 0.f;
@@ -1177,12 +1178,12 @@ cudaError_t launch_prefill_bf16(const PrefillParams& p, cudaStream_t stream) {
     q.head_group = (int)hg;
   }
   if (p.cache_dtype == PKV_I8)
-    return p.lse ? launch_codes<PKV_I8, true>(grid, tq, q, stream) : launch_codes<PKV_I8, false>(grid, tq, q, stream);
+    return p.neg_lse ? launch_codes<PKV_I8, true>(grid, tq, q, stream) : launch_codes<PKV_I8, false>(grid, tq, q, stream);
   if (p.cache_dtype == PKV_E4M3)
-    return p.lse ? launch_codes<PKV_E4M3, true>(grid, tq, q, stream)
+    return p.neg_lse ? launch_codes<PKV_E4M3, true>(grid, tq, q, stream)
                  : launch_codes<PKV_E4M3, false>(grid, tq, q, stream);
   if (p.paged)
-    return p.lse ? launch_variant<true, false, true>(grid, tq, tk, tv, q, stream)
+    return p.neg_lse ? launch_variant<true, false, true>(grid, tq, tk, tv, q, stream)
                  : launch_variant<true, false, false>(grid, tq, tk, tv, q, stream);
   if (f8) return launch_variant<false, true, false>(grid, tq, tk, tv, q, stream);
   return launch_variant<false, false, false>(grid, tq, tk, tv, q, stream);
