@@ -50,11 +50,11 @@
 // and e4m3 codes are exact in bf16, so the MMAs run on bf16 codes and the scales
 // are applied in float32: a key block's scale joins the softmax scale, a value
 // block's scale multiplies P before it is rounded to bf16.  A fourth warpgroup
-// joins and warps 10-15 take the place of the TMA loads: the tiles' 16-row pieces
-// (a piece lies in one page and one scale block) go round the six warps, each of
+// joins and warps 8 and 10-15 take the place of the TMA loads: the tiles' 16-row pieces
+// (a piece lies in one page and one scale block) go round the seven warps, each of
 // which copies its next pieces with cp.async, converts the codes in registers and
 // writes the swizzled bf16 tile that TMA would have written.  A lane converts
-// exactly the bytes it copied, so a piece needs no barrier.  Warp 10 also does the
+// exactly the bytes it copied, so a piece needs no barrier.  Warp 8 also does the
 // loader's other work (Q loads, item claims); rows past the sequence and rows of
 // bad pages are written as zeros.  Two converting warps (in the two idle ones) took
 // 10500 cycles a tile, as one warp issues a dependent instruction every four
@@ -131,7 +131,7 @@ constexpr int kSmemBytes = kSmemUsed + 1024;       // slack for 1024-byte alignm
 // 8-bit caches: scales of the K/V tiles in flight, then each converter warp's
 // ring of 2 KB pieces (16 rows of 128 codes).
 constexpr int kScaleSlots = 8;
-constexpr int kConverters = 6;                                     // warps 10 .. 15
+constexpr int kConverters = 7;                                     // warps 8 and 10 .. 15
 constexpr int kPieces = 2;                                         // of a warp's pieces in its ring
 constexpr int kPieceBytes = 16 * D;
 constexpr int kOffScale = (kSmemUsed + 15) & ~15;                  // float[kScaleSlots][16]: 8 ks, 8 vs
@@ -320,22 +320,21 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUten
 
   if (warp >= 8) regs_decrease<kQ8 ? kRegsSideQ8 : kRegsSide>();
 
-  if (kQ8 && warp >= 10) {
+  if (kQ8 && warp >= 8 && warp != 9) {
     // ------------------------------------------- loader and converters, 8-bit --
-    const int part = warp - 10;                      // takes pieces part, part + kConverters, ...
+    const int part = warp == 8 ? 0 : warp - 9;       // takes pieces part, part + kConverters, ...
     const bool lead = part == 0;                     // loads Q and claims items
     const uint32_t ring = sbase + kOffPiece + part * kPieces * kPieceBytes + lane * 16;
     const uint8_t* raw0 = smem + kOffPiece + part * kPieces * kPieceBytes + lane * 16;
     float* scales = reinterpret_cast<float*>(smem + kOffScale);
-    const int ck = lane & 7, rk = lane >> 3;         // this lane's 16-byte chunk, and row + 4 u
+    // This lane's 16-byte chunk of codes, and row + 4 u.  Eight lanes take four
+    // chunks of two rows: what they write then falls into eight bank groups.
+    const int ck = (lane & 3) + ((lane >> 3) & 1) * 4, rk = ((lane >> 2) & 1) + (lane >> 4) * 2;
     const int stride = p.H_kv * D;
-    // where this lane's codes go in a tile: chunks 2c, 2c + 1 of a row's 64-column
-    // block, by the row's swizzle.  The lanes of the second block store them the
-    // other way round, so that eight lanes meet eight bank groups.
-    const bool swap = ck >= 4;
+    // its bf16 chunks 2c, 2c + 1 in a row's 64-column block, by the row's swizzle
     const int col = (ck >> 2) * kHalfBytes + rk * 128;
-    const int at0 = ((2 * (ck & 3) + swap) ^ rk) << 4;              // rows rk, rk + 8; rows rk + 4, + 12: ^ 64
-    const int at1 = ((2 * (ck & 3) + !swap) ^ rk) << 4;
+    const int at0 = ((2 * (ck & 3)) ^ rk) << 4;      // rows rk, rk + 8; rows rk + 4, + 12: ^ 64
+    const int at1 = ((2 * (ck & 3) + 1) ^ rk) << 4;
     int kv_it = 0, claims = 0;
     int q_it[kQTiles] = {0, 0};
     uint32_t q_pend = 0;                             // Q tile t: bit t loads pending, bit 2 + t their parity
@@ -431,8 +430,8 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUten
           codes_to_bf16<kCache>(x.y, a.z, a.w);
           codes_to_bf16<kCache>(x.z, b.x, b.y);
           codes_to_bf16<kCache>(x.w, b.z, b.w);
-          *reinterpret_cast<uint4*>(tile + u * 512 + (at0 ^ ((u & 1) << 6))) = swap ? b : a;
-          *reinterpret_cast<uint4*>(tile + u * 512 + (at1 ^ ((u & 1) << 6))) = swap ? a : b;
+          *reinterpret_cast<uint4*>(tile + u * 512 + (at0 ^ ((u & 1) << 6))) = a;
+          *reinterpret_cast<uint4*>(tile + u * 512 + (at1 ^ ((u & 1) << 6))) = b;
         }
         fence_proxy_async_smem();
         mbar_arrive(bar((is_v ? kBarVFull : kBarKFull) + st));
