@@ -78,15 +78,23 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_device(*tensors):
     """A context in which the tensors' device is current (nothing to do if it is)."""
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        _need(t.is_cuda and t.device == dev, "every tensor must be on one CUDA device")
-        _need(t.is_contiguous(), "every tensor must be contiguous")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("every tensor must be on one CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("every tensor must be contiguous")
+    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_of(stream, t):
+    """The stream's address: None means the current stream of the tensor's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else B._stream(stream)
 
 
 def _pools(k_pages, v_pages, k_scales, v_scales):
@@ -143,7 +151,7 @@ def append_q8(k_new, v_new, cu_new, start_pos, block_table, k_pages, v_pages, k_
     with _on_device(k_pages, v_pages, k_scales, v_scales, k_new, v_new, cu_new, start_pos, block_table):
         B.paged_kv_append_q8(k_new, v_new, cu_new, start_pos, block_table, block_table.shape[1], S,
                              k_new.shape[0], k_pages, v_pages, k_scales, v_scales, P, ps, block, H_kv, d,
-                             _dtype(k_new), cache, stream)
+                             _dtype(k_new), cache, _stream_of(stream, k_pages))
 
 
 def copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None) -> None:
@@ -156,7 +164,7 @@ def copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, stream=None) -
     _need(src.shape == dst.shape, "as many sources as destinations")
     with _on_device(k_pages, v_pages, k_scales, v_scales, src, dst):
         B.paged_kv_copy_pages_q8(k_pages, v_pages, k_scales, v_scales, src, dst, src.numel(), P, ps, block, H_kv,
-                                 d, cache, stream)
+                                 d, cache, _stream_of(stream, k_pages))
 
 
 def _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out):
@@ -184,7 +192,7 @@ def paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, pag
                            q.device)
         B.paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S, q_len,
                         H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale, cache, o,
-                        ws, n, stream)
+                        ws, n, _stream_of(stream, q))
         _used_on(stream, o, ws)
     return o
 
@@ -204,7 +212,7 @@ def paged_weights(q, k_pages, v_pages, block_table, seq_lens, page_size: int, ca
                            q.device)
         B.paged_attn_weights(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S,
                              q_len, H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale,
-                             cache, o, weights, weights.shape[2], ws, n, stream)
+                             cache, o, weights, weights.shape[2], ws, n, _stream_of(stream, q))
         _used_on(stream, o, ws)
     return o
 
@@ -234,6 +242,6 @@ def evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, recent:
         ws, n = _workspace(workspace, B.paged_kv_evict_workspace_size(S, H_kv, budget, block, cache), k_pages.device)
         B.paged_kv_evict(k_pages, v_pages, k_scales, v_scales, weights, weights_out, weights.shape[2], block_table,
                          dst_table, seq_lens, new_lens, kept, budget, recent, S, H_kv, d, P, ps, block,
-                         block_table.shape[1], max_seq_len, cache, ws, n, stream)
+                         block_table.shape[1], max_seq_len, cache, ws, n, _stream_of(stream, k_pages))
         _used_on(stream, kept, new_lens, ws)
     return kept, new_lens

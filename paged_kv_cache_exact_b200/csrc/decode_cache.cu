@@ -56,6 +56,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSplitPages = 256;               // table entries staged per CTA (16-token pages)
 constexpr int kMaxSplitTokens = 4096;
+constexpr int kOneSplit = 512;
 constexpr int kMaxSplits = 1024;
 
 // d[16x8] += a[16x16] * b[16x8], f32 accumulation
@@ -533,9 +534,7 @@ PKV_DEVINLINE void merge_ml(const float2* ml, int nsplit, int lane, float& M, fl
 
 // Splits -> output: one warp per (sequence, head), lane i owns head dims 4i .. 4i+3.
 constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const CacheAttnParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long sh = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+PKV_DEVINLINE void merge_rows(const CacheAttnParams& p, long long sh) {
   const int lane = threadIdx.x & 31;
   if (sh >= (long long)p.num_seqs * p.H) return;
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
@@ -563,18 +562,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) cache_merge_kernel(const Cac
   out[1] = __floats2bfloat162_rn(none ? 0.f : acc.z / lsum, none ? 0.f : acc.w / lsum);
 }
 
-// Scores -> weights: grid = (token ranges, kv head, sequence).  Each thread owns
-// tokens; a token's weight is the sum over the group's heads of 2^(x - lse).
+// Scores -> weights, for a range of a sequence's tokens and a kv head.  Each thread
+// owns tokens; a token's weight is the sum over the group's heads of 2^(x - lse).
 constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;               // tokens a CTA
 constexpr int kMaxGroup = 256;                    // query heads per kv head
-__global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const CacheAttnParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, int s) {
   __shared__ float s_lse[kMaxGroup];
-  const int kvh = blockIdx.y, s = blockIdx.z;
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
   const int L = max(0, min(p.seq_lens[s], cap));
-  const int t0 = blockIdx.x * kWeightTokens;
+  const int t0 = range * kWeightTokens;
   if (t0 >= L) return;
   const int group = p.H / p.H_kv;
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
@@ -601,6 +598,21 @@ __global__ void __launch_bounds__(kWeightThreads) cache_weights_kernel(const Cac
     }
     w[t] += sum;
   }
+}
+
+// What follows the split kernel, in one launch: the first p.merge_ctas CTAs merge
+// splits, a warp a (sequence, head); the others take the weights' ranges.
+static_assert(kMergeWarps * 32 == kWeightThreads, "one block size");
+__global__ void __launch_bounds__(kWeightThreads) cache_finish_kernel(const CacheAttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x < p.merge_ctas) {
+    merge_rows(p, (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5));
+    return;
+  }
+  const int ranges = (p.max_seq_len + kWeightTokens - 1) / kWeightTokens;
+  const int i = blockIdx.x - p.merge_ctas;
+  const int pair = i / ranges;
+  range_weights(p, i - pair * ranges, pair % p.H_kv, pair / p.H_kv);
 }
 
 template <int kCache, int NT, bool kWeights>
@@ -658,6 +670,9 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
   const int heads = group > 8 ? 16 : 8;
   const long long pairs = (long long)num_seqs * H_kv * ((group + heads - 1) / heads);
   int st = 64 < page_size ? page_size : 64;
+  // Short contexts: one split, as the merge's launch costs more than the splits
+  // save (one sequence of 437 tokens, 8 kv heads: 10.4 us in 7 splits).
+  if (max_seq_len <= kOneSplit) st = kOneSplit;
   // Double while at least 8 CTAs per SM remain.  A split writes (and the merge
   // reads) 512 bytes per query head: with few heads that is little, and shorter
   // splits balance ragged lengths better (64 sequences x 32 heads, int8: 441 us at
@@ -679,17 +694,13 @@ cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
   else
     e = w ? launch_decode<PKV_BF16, true>(p, stream) : cudaErrorNotSupported;
   if (e != cudaSuccess) return e;
-  if (p.max_splits > 1) {
-    const long long rows = (long long)p.num_seqs * p.H;
-    e = launch_after(cache_merge_kernel, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
-                     kMergeWarps * 32, p, stream);
-    if (e != cudaSuccess) return e;
-  }
-  if (w)
-    e = launch_after(cache_weights_kernel,
-                     dim3((p.max_seq_len + kWeightTokens - 1) / kWeightTokens, p.H_kv, p.num_seqs),
-                     kWeightThreads, p, stream);
-  return e;
+  CacheAttnParams q = p;
+  q.merge_ctas = 0;
+  if (p.max_splits > 1) q.merge_ctas = (int)(((long long)p.num_seqs * p.H + kMergeWarps - 1) / kMergeWarps);
+  long long ctas = q.merge_ctas;
+  if (w) ctas += (long long)((p.max_seq_len + kWeightTokens - 1) / kWeightTokens) * p.H_kv * p.num_seqs;
+  if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;
+  return ctas ? launch_after(cache_finish_kernel, dim3((unsigned)ctas), kWeightThreads, q, stream) : cudaSuccess;
 }
 
 }  // namespace pkv
