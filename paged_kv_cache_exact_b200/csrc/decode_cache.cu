@@ -135,7 +135,7 @@ cache_decode_kernel(const CacheAttnParams p) {
   constexpr int U = Lay::kUnroll;
   extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][piece][lane] 16 bytes
   __shared__ int s_pages[kMaxSplitPages];
-  __shared__ float2 s_scale[kBf16 ? 1 : kMaxSplitTokens / 16];   // (ks, vs) of every chunk
+  __shared__ __align__(8) float s_scale[kWarps][Lay::kStages][U][2];      // (ks, vs) of the chunks in the ring
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -149,6 +149,15 @@ cache_decode_kernel(const CacheAttnParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
 
+  // The split's table entries are fetched along with the length: what lies past the
+  // sequence is not looked at.
+  const int t_begin = split * p.split_tokens;
+  const int lp0 = t_begin >> p.page_shift;
+  const int n_lp = min(p.max_pages - lp0, (p.split_tokens + p.page_size - 1) >> p.page_shift);
+  int mine_lp[kMaxSplitPages / kThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxSplitPages / kThreads; ++i)
+    mine_lp[i] = tid + i * kThreads < n_lp ? p.block_table[(size_t)s * p.max_pages + lp0 + tid + i * kThreads] : -1;
   int L = p.seq_lens[s];
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
   if (L < 1 || L > cap) {
@@ -161,20 +170,19 @@ cache_decode_kernel(const CacheAttnParams p) {
         p.out[((size_t)s * p.H + h0) * D + i] = __float2bfloat16_rn(0.f);
     return;
   }
-  const int t_begin = split * p.split_tokens;
   if (t_begin >= L) return;
   const int t_end = min(L, t_begin + p.split_tokens);
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
-
-  const int lp0 = t_begin >> p.page_shift;
   const int lp1 = (t_end - 1) >> p.page_shift;
-  for (int i = tid; i <= lp1 - lp0; i += kThreads) {
-    int phys = p.block_table[(size_t)s * p.max_pages + lp0 + i];
+#pragma unroll
+  for (int i = 0; i < kMaxSplitPages / kThreads; ++i) {
+    int phys = mine_lp[i];
+    if (tid + i * kThreads > lp1 - lp0) break;
     if (phys < 0 || phys >= p.num_pages) {
       flag_error(p.err, PKV_DEVERR_BAD_PAGE);
       phys = -1;
     }
-    s_pages[i] = phys;
+    s_pages[tid + i * kThreads] = phys;
   }
 
   // Q^T as the B operand: column n = g is head g, and each lane holds the head
@@ -265,18 +273,17 @@ cache_decode_kernel(const CacheAttnParams p) {
   auto prefetch_step = [&](int c, int st) {                  // chunks c, c + kWarps, ...
 #pragma unroll
     for (int u = 0; u < U; ++u) prefetch(c + u * kWarps, mine + st * Lay::kStageBytes + u * Lay::kChunkBytes);
+    if (!kBf16 && lane < 2 * U) {                            // a lane a scale: K's and V's of each chunk
+      bool ok;
+      const size_t at = (chunk_row(c + (lane >> 1) * kWarps, ok) >> p.block_shift) * p.H_kv + kvh;
+      float* to = &s_scale[warp][st][lane >> 1][lane & 1];
+      if (ok) cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(to)), ((lane & 1) ? p.v_scales : p.k_scales) + at);
+      else *to = 1.f;
+    }
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < Lay::kStages - 1; ++i) prefetch_step(warp + i * kWarps * U, i);
-  if (!kBf16) {
-    for (int c = tid; c < n_chunks; c += kThreads) {
-      bool ok;
-      const size_t at = (chunk_row(c, ok) >> p.block_shift) * p.H_kv + kvh;
-      if (ok) s_scale[c] = make_float2(p.k_scales[at], p.v_scales[at]);
-    }
-    __syncthreads();
-  }
 
   float o[NT][8][4];
   float m[NT][2], l[NT][2];
@@ -295,6 +302,7 @@ cache_decode_kernel(const CacheAttnParams p) {
     cp_async_wait<Lay::kStages - 1>();
     __syncwarp();                                            // every lane's copies have landed
     const uint8_t* stage = ring + (warp * Lay::kStages + st) * Lay::kStageBytes;
+    const int now = st;
     st = st == Lay::kStages - 1 ? 0 : st + 1;
     // K: rows g and g + 8, 16-byte pieces t4, t4 + 4, ...; V: piece g (and g + 8)
     // of rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
@@ -325,7 +333,7 @@ cache_decode_kernel(const CacheAttnParams p) {
       const int cu = c + u * kWarps;
       tok[u] = t_begin + 16 * cu;
       page_ok[u] = cu < n_chunks && s_pages[(tok[u] >> p.page_shift) - lp0] >= 0;
-      scales[u] = kBf16 || !page_ok[u] ? make_float2(1.f, 1.f) : s_scale[kBf16 ? 0 : cu];
+      scales[u] = kBf16 ? make_float2(1.f, 1.f) : *reinterpret_cast<const float2*>(s_scale[warp][now][u]);
     }
     // S^T = K Q^T, in two chains of four steps
     float sc[U][NT][4], sd[U][NT][4];
