@@ -126,13 +126,16 @@ struct Layout {
   static constexpr float kLift = kBf16 ? 0.f : 7.f;
 };
 
-template <int kCache, int NT, bool kWeights>
+// kOne: one query head per kv head; a lane then works on column 2 t4 alone (the
+// real one is column 0, of lanes t4 = 0).
+template <int kCache, int NT, bool kWeights, bool kOne>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 cache_decode_kernel(const CacheAttnParams p) {
   using Lay = Layout<kCache>;
   constexpr bool kBf16 = Lay::kBf16;
   constexpr int kHeads = 8 * NT;
   constexpr int U = Lay::kUnroll;
+  constexpr int J = kOne ? 1 : 2;                            // columns of a lane
   extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][piece][lane] 16 bytes
   __shared__ int s_pages[kMaxSplitPages];
   __shared__ __align__(8) float s_scale[kWarps][Lay::kStages][U][2];      // (ks, vs) of the chunks in the ring
@@ -368,14 +371,14 @@ cache_decode_kernel(const CacheAttnParams p) {
       const bool in0 = page_ok[u] && tok[u] + g < t_end, in1 = page_ok[u] && tok[u] + g + 8 < t_end;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = hm[nt][0] * scales[u].x, f1 = hm[nt][1] * scales[u].x;
         float (&x)[4] = sc[u][nt];
-        x[0] = in0 ? (x[0] + sd[u][nt][0]) * f0 : -INFINITY;
-        x[1] = in0 ? (x[1] + sd[u][nt][1]) * f1 : -INFINITY;
-        x[2] = in1 ? (x[2] + sd[u][nt][2]) * f0 : -INFINITY;
-        x[3] = in1 ? (x[3] + sd[u][nt][3]) * f1 : -INFINITY;
-        passed = passed || fmaxf(x[0], x[2]) > m[nt][0] + (Lay::kLift + 8.f) ||
-                 fmaxf(x[1], x[3]) > m[nt][1] + (Lay::kLift + 8.f);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float f = hm[nt][j] * scales[u].x;
+          x[j] = in0 ? (x[j] + sd[u][nt][j]) * f : -INFINITY;
+          x[2 + j] = in1 ? (x[2 + j] + sd[u][nt][2 + j]) * f : -INFINITY;
+          passed = passed || fmaxf(x[j], x[2 + j]) > m[nt][j] + (Lay::kLift + 8.f);
+        }
       }
       if (kWeights) {
         // [S, H_kv, tokens, group]; tokens past the sequence are not written
@@ -400,7 +403,7 @@ cache_decode_kernel(const CacheAttnParams p) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < J; ++j) {
           float mx = fmaxf(sc[0][nt][j], sc[0][nt][2 + j]);
 #pragma unroll
           for (int u = 1; u < U; ++u) mx = fmaxf(mx, fmaxf(sc[u][nt][j], sc[u][nt][2 + j]));
@@ -424,16 +427,18 @@ cache_decode_kernel(const CacheAttnParams p) {
     uint32_t pb[U][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float s0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-      const float s1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float p0 = ex2(sc[u][nt][0] - s0), p1 = ex2(sc[u][nt][1] - s1);
-        const float p2 = ex2(sc[u][nt][2] - s0), p3 = ex2(sc[u][nt][3] - s1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pb[u][nt][0] = transpose8x8(kBf16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1));
-        pb[u][nt][1] = transpose8x8(kBf16 ? pack_bf16x2(p2, p3) : pack_f16x2(p2, p3));
+        float pr[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const float ref = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+          pr[j] = ex2(sc[u][nt][j] - ref);
+          pr[2 + j] = ex2(sc[u][nt][2 + j] - ref);
+          l[nt][j] += pr[j] + pr[2 + j];
+        }
+        pb[u][nt][0] = transpose8x8(kBf16 ? pack_bf16x2(pr[0], pr[1]) : pack_f16x2(pr[0], pr[1]));
+        pb[u][nt][1] = transpose8x8(kBf16 ? pack_bf16x2(pr[2], pr[3]) : pack_f16x2(pr[2], pr[3]));
       }
     }
     // O^T += vs V^T P^T
@@ -469,9 +474,15 @@ cache_decode_kernel(const CacheAttnParams p) {
               float acc[4] = {0.f, 0.f, 0.f, 0.f};
               mma16816<true>(acc, a[2 * e], a[2 * e + 1], b[2 * e], b[2 * e + 1], pb[u][nt][0], pb[u][nt][1]);
 #pragma unroll
-              for (int q = 0; q < 4; q += 2) {
-                float* oo = &o[nt][2 * w + e][q];
-                unf2(fma2(f2(vs, vs), f2(acc[q], acc[q + 1]), f2(oo[0], oo[1])), oo[0], oo[1]);
+              if (kOne) {
+                float (&oo)[4] = o[nt][2 * w + e];
+                unf2(fma2(f2(vs, vs), f2(acc[0], acc[2]), f2(oo[0], oo[2])), oo[0], oo[2]);
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                  float* oo = &o[nt][2 * w + e][q];
+                  unf2(fma2(f2(vs, vs), f2(acc[q], acc[q + 1]), f2(oo[0], oo[1])), oo[0], oo[1]);
+                }
               }
             }
         }
@@ -486,7 +497,7 @@ cache_decode_kernel(const CacheAttnParams p) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < J; ++j) {
       float v = l[nt][j];
       v += __shfl_xor_sync(0xffffffffu, v, 4);
       v += __shfl_xor_sync(0xffffffffu, v, 8);
@@ -623,7 +634,7 @@ __global__ void __launch_bounds__(kWeightThreads) cache_finish_kernel(const Cach
   range_weights(p, i - pair * ranges, pair % p.H_kv, pair / p.H_kv);
 }
 
-template <int kCache, int NT, bool kWeights>
+template <int kCache, int NT, bool kWeights, bool kOne>
 cudaError_t launch_split(const CacheAttnParams& p, dim3 grid, cudaStream_t stream) {
   // The shared-memory limit is an attribute per device; host threads may get
   // here at once, so the once-per-device record is kept under a lock.
@@ -635,13 +646,13 @@ cudaError_t launch_split(const CacheAttnParams& p, dim3 grid, cudaStream_t strea
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(cache_decode_kernel<kCache, NT, kWeights>,
+      e = cudaFuncSetAttribute(cache_decode_kernel<kCache, NT, kWeights, kOne>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kCache>::kRingBytes);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  cache_decode_kernel<kCache, NT, kWeights><<<grid, kThreads, Layout<kCache>::kRingBytes, stream>>>(p);
+  cache_decode_kernel<kCache, NT, kWeights, kOne><<<grid, kThreads, Layout<kCache>::kRingBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -650,8 +661,9 @@ cudaError_t launch_decode(const CacheAttnParams& p, cudaStream_t stream) {
   const int group = p.H / p.H_kv;
   const int heads = group > 8 ? 16 : 8;
   const dim3 grid(p.H_kv * ((group + heads - 1) / heads), p.max_splits, p.num_seqs);
-  return group > 8 ? launch_split<kCache, 2, kWeights>(p, grid, stream)
-                   : launch_split<kCache, 1, kWeights>(p, grid, stream);
+  if (group > 8) return launch_split<kCache, 2, kWeights, false>(p, grid, stream);
+  return group > 1 ? launch_split<kCache, 1, kWeights, false>(p, grid, stream)
+                   : launch_split<kCache, 1, kWeights, true>(p, grid, stream);
 }
 
 // The kernel after the split kernel, as its programmatic dependent: it may be
