@@ -34,9 +34,6 @@
 namespace pkv {
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kMoveThreads = 256;
 // rows a thread has in flight: what fits 64 registers (four CTAs an SM)
 template <int kCache> constexpr int move_unroll() { return kCache == PKV_BF16 ? 8 : 4; }
 
@@ -78,9 +75,10 @@ PKV_DEVINLINE uint32_t warp_scan(uint32_t v, int lane) {           // inclusive
   return v;
 }
 
-// kKeys: tokens a thread holds.
-template <int kKeys>
-__global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictParams p) {
+// kKeys: tokens a thread holds; kSelectThreads: threads of the CTA.
+template <int kKeys, int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_kernel(const EvictParams p) {
+  constexpr int kSelectWarps = kSelectThreads / 32;
   extern __shared__ uint32_t words[];               // a segment's keys, then its kept tokens
   __shared__ __align__(16) int hist[256];
   __shared__ uint32_t s_lo[kSelectWarps], s_hi[kSelectWarps], s_count[kSelectWarps];
@@ -137,8 +135,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) s_lo[warp] = lo, s_hi[warp] = hi;
     __syncthreads();
-    lo = __reduce_min_sync(0xffffffffu, s_lo[lane]);
-    hi = __reduce_max_sync(0xffffffffu, s_hi[lane]);
+    lo = __reduce_min_sync(0xffffffffu, s_lo[lane % kSelectWarps]);
+    hi = __reduce_max_sync(0xffffffffu, s_hi[lane % kSelectWarps]);
     // The threshold is the `need`-th largest of the keys that agree with `threshold`
     // from bit `shift` on; keys larger than those are counted out of `need` already.
     need = pick;
@@ -147,7 +145,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
     while (shift > 0) {
       const int bits = min(shift, 8);
       shift -= bits;
-      if (tid < 256) hist[tid] = 0;
+      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
       __syncthreads();
       each([&](uint32_t k) {
         const uint32_t d = (k ^ threshold) >> shift;                 // threshold has zeros in this digit and below
@@ -201,7 +199,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
     const uint32_t in_warp = warp_scan(n, lane);
     if (lane == 31) s_count[warp] = in_warp;
     __syncthreads();
-    const uint32_t warps = warp_scan(s_count[lane], lane);
+    const uint32_t warps = warp_scan(lane < kSelectWarps ? s_count[lane] : 0u, lane);
     const uint32_t total = __shfl_sync(0xffffffffu, warps, 31);
     const uint32_t before = (warp ? __shfl_sync(0xffffffffu, warps, warp - 1) : 0u) + in_warp - n;
     const int first = base_gt + min(base_eq, need);                 // where this segment's kept tokens start
@@ -266,6 +264,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const EvictPa
 }
 
 // The weights of one (sequence, head), by the same rule as its rows.
+template <int kMoveThreads>
 PKV_DEVINLINE void move_weights(const EvictParams& p) {
   constexpr int kUnroll = 8;
   const int h = blockIdx.y, s = blockIdx.z;
@@ -291,12 +290,12 @@ PKV_DEVINLINE void move_weights(const EvictParams& p) {
   for (int t = m + threadIdx.x; t < L; t += kMoveThreads) wo[t] = 0.f;
 }
 
-template <int kCache>
-__global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams p) {
+template <int kCache, int kMoveThreads>
+__global__ void __launch_bounds__(kMoveThreads, 1024 / kMoveThreads) move_kernel(const EvictParams p) {
   constexpr int kMoveUnroll = move_unroll<kCache>();
   const int slices = p.row_bytes / p.slice_bytes;
   if ((int)blockIdx.x == 2 * slices) {
-    move_weights(p);
+    move_weights<kMoveThreads>(p);
     return;
   }
   const bool is_v = (int)blockIdx.x >= slices;
@@ -365,11 +364,24 @@ __global__ void __launch_bounds__(kMoveThreads, 4) move_kernel(const EvictParams
   }
 }
 
-template <int kKeys>
+// At most 64 registers: an SM holds four CTAs of 256 threads or eight of 128.  The
+// wide ones have more rows in flight where all CTAs run at once; beyond that the
+// narrow ones waste less of the last turn (1280 CTAs, 32 sequences x 8 heads: 100
+// us against 105; 576 CTAs, 8 long sequences: 94 against 68).
+template <int kCache>
+cudaError_t launch_move(const EvictParams& p, dim3 grid, cudaStream_t stream) {
+  if ((long long)grid.x * grid.y * grid.z <= 148LL * 4)
+    move_kernel<kCache, 256><<<grid, 256, 0, stream>>>(p);
+  else
+    move_kernel<kCache, 128><<<grid, 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int kKeys, int kSelectThreads>
 cudaError_t launch_select(const EvictParams& p, dim3 grid, cudaStream_t stream) {
   // The shared-memory limit is an attribute per device; host threads may get
   // here at once, so the once-per-device record is kept under a lock.
-  constexpr int kSmem = (kKeys * kSelectThreads + kKeys * kSelectWarps) * 4;
+  constexpr int kSmem = (kKeys * kSelectThreads + kKeys * kSelectThreads / 32) * 4;
   static bool done[64] = {};
   static std::mutex mu;
   int dev = 0;
@@ -378,12 +390,12 @@ cudaError_t launch_select(const EvictParams& p, dim3 grid, cudaStream_t stream) 
   {
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-      e = cudaFuncSetAttribute(select_kernel<kKeys>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      e = cudaFuncSetAttribute((select_kernel<kKeys, kSelectThreads>), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  select_kernel<kKeys><<<grid, kSelectThreads, kSmem, stream>>>(p);
+  select_kernel<kKeys, kSelectThreads><<<grid, kSelectThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -391,10 +403,13 @@ cudaError_t launch_select(const EvictParams& p, dim3 grid, cudaStream_t stream) 
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   const dim3 rows(p.H_kv, p.num_seqs);
-  // registers for the longest sequence's weights: 4, 16 or 32 a thread
-  cudaError_t e = p.max_seq_len <= 4 * kSelectThreads    ? launch_select<4>(p, rows, stream)
-                  : p.max_seq_len <= 16 * kSelectThreads ? launch_select<16>(p, rows, stream)
-                                                         : launch_select<32>(p, rows, stream);
+  // Registers for the longest sequence's weights, and no more threads than that
+  // takes: barriers are cheaper and more CTAs fit an SM.
+  cudaError_t e = p.max_seq_len <= 1024    ? launch_select<4, 256>(p, rows, stream)
+                  : p.max_seq_len <= 4096  ? launch_select<16, 256>(p, rows, stream)
+                  : p.max_seq_len <= 8192  ? launch_select<16, 512>(p, rows, stream)
+                  : p.max_seq_len <= 16384 ? launch_select<16, 1024>(p, rows, stream)
+                                           : launch_select<32, 1024>(p, rows, stream);
   if (e != cudaSuccess) return e;
   // Wide slices make whole 128-byte requests; narrow ones make more CTAs of few
   // (sequence, head) pairs.  Halve while there are fewer than 4 CTAs per SM.
@@ -402,10 +417,9 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   q.slice_bytes = p.row_bytes < 128 ? p.row_bytes : 128;
   while (q.slice_bytes > 32 && 2LL * p.row_bytes / q.slice_bytes * p.H_kv * p.num_seqs < 148LL * 4) q.slice_bytes /= 2;
   const dim3 grid(2 * p.row_bytes / q.slice_bytes + 1, p.H_kv, p.num_seqs);      // + the weights
-  if (p.cache_dtype == PKV_I8) move_kernel<PKV_I8><<<grid, kMoveThreads, 0, stream>>>(q);
-  else if (p.cache_dtype == PKV_E4M3) move_kernel<PKV_E4M3><<<grid, kMoveThreads, 0, stream>>>(q);
-  else move_kernel<PKV_BF16><<<grid, kMoveThreads, 0, stream>>>(q);
-  return cudaGetLastError();
+  if (p.cache_dtype == PKV_I8) return launch_move<PKV_I8>(q, grid, stream);
+  if (p.cache_dtype == PKV_E4M3) return launch_move<PKV_E4M3>(q, grid, stream);
+  return launch_move<PKV_BF16>(q, grid, stream);
 }
 
 }  // namespace pkv

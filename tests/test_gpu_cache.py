@@ -164,6 +164,19 @@ def test_decode_accumulates_weights(dtype, case):
     assert torch.equal(c.w, mid)
 
 
+@pytest.mark.parametrize("H,H_kv", [(8, 8), (16, 2), (9, 3)])
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+def test_decode_of_a_ragged_batch(dtype, H, H_kv):
+    """Enough sequences that splits grow long, some of them one token."""
+    r = random.Random(H)
+    c = Cache(dtype, [r.choice([1, r.randint(2, 600), r.randint(600, 4500)]) for _ in range(60)] + [4500], H, H_kv,
+              32, 16, seed=H)
+    before = c.w.clone()
+    c.check(c.run(True), before)
+    if dtype != BF16:
+        c.check(c.run(False))
+
+
 def test_weights_of_a_step_sum_to_the_query_heads():
     c = Cache(I8, [5, 1200], 16, 4, 32, 16)
     c.w.zero_()
@@ -587,6 +600,12 @@ EVICT = [
     ([2500, 40, 1024], 1024, 10, 2, 64, 16),     # longer than one sweep of the selection; exactly the budget
     ([3000], 1100, 33, 2, 256, 128),             # more than one chunk of rows
     ([1025, 700], 1, 1, 1, 128, 64),
+    # the selection's other sizes: more than 4096, 8192, 16384 tokens, and rows read in several segments
+    ([5000, 4097], 700, 100, 1, 64, 32),
+    ([9000, 12], 2000, 0, 1, 256, 256),
+    ([20000], 9000, 8999, 1, 128, 16),
+    ([70000, 33000], 33500, 500, 1, 256, 64),
+    ([37 * (i % 5) + i for i in range(60)], 50, 7, 6, 16, 16),      # many pairs: narrow CTAs, wide slices
 ]
 
 
