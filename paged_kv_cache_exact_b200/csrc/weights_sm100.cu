@@ -14,12 +14,16 @@
 // Bound: 128 x 128 exponentials take 1024 cycles of an SM's MUFU, the tile's MMA
 // half of that, so the MMA and the loads hide behind the exponentials.  Warp 0
 // streams Q tiles and their lse by TMA (4 stages), warp 1 issues the MMAs into 4
-// TMEM buffers, and four epilogue warpgroups take the tiles in turn, each with a
-// buffer of its own: four warps a scheduler cover one another's TMEM and
-// exponential latencies (two groups: 190 us for 32 heads of 4096 causal rows).
+// TMEM buffers, and three epilogue warpgroups take the tiles in turn; a warp loads
+// the next quarter of its tile from TMEM while it sums this one, and a quarter of
+// the exponentials is computed on the FMA pipe, which is idle otherwise.  With the
+// attention before it, 32 heads of 4096 causal rows: two groups 315 us, four 288,
+// the first keys of every head first 241, then three groups with the loads ahead
+// 239 and with the FMA pipe's share 231.
 #include <cuda.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "cache_attn.cuh"
 #include "q8.cuh"
@@ -35,7 +39,7 @@ constexpr int BK = 128;                 // keys per CTA
 constexpr int BQ = 128;                 // query rows per tile
 constexpr int kStages = 4;              // Q ring depth
 constexpr int kBufs = 4;                // S^T buffers in TMEM
-constexpr int kEpiGroups = 4;           // epilogue warpgroups
+constexpr int kEpiGroups = 3;           // epilogue warpgroups
 constexpr int kEpiWarps = 4 * kEpiGroups;
 constexpr int kThreads = (kEpiWarps + 4) * 32;
 constexpr int kTileBytes = BQ * D * 2;  // 32 KB
@@ -59,6 +63,35 @@ PKV_DEVINLINE void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+PKV_DEVINLINE float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// acc += 2^x for a pair: x = n + f with n the nearest integer, 2^f by the degree-5
+// polynomial that interpolates it at the Chebyshev nodes of [-1/2, 1/2] (relative
+// error 2.2e-7 in float32), 2^n by its exponent bits.  Below 2^-126 it gives 2^-126,
+// which is nothing to a sum of weights; NaN stays NaN.
+PKV_DEVINLINE uint64_t exp2_pair_add(uint64_t x2, uint64_t acc) {
+  float a, b;
+  unf2(x2, a, b);
+  x2 = f2(max_nan(a, -126.f), max_nan(b, -126.f));
+  const uint64_t t = add2(x2, f2(12582912.f, 12582912.f));         // 1.5 * 2^23 + n
+  const uint64_t f = sub2(x2, sub2(t, f2(12582912.f, 12582912.f)));
+  uint64_t y = f2(0x1.5f0890p-10f, 0x1.5f0890p-10f);
+  y = fma2(y, f, f2(0x1.3d1070p-7f, 0x1.3d1070p-7f));
+  y = fma2(y, f, f2(0x1.c6af6cp-5f, 0x1.c6af6cp-5f));
+  y = fma2(y, f, f2(0x1.ebf906p-3f, 0x1.ebf906p-3f));
+  y = fma2(y, f, f2(0x1.62e430p-1f, 0x1.62e430p-1f));
+  y = fma2(y, f, f2(0x1.000002p+0f, 0x1.000002p+0f));
+  float ta, tb;
+  unf2(t, ta, tb);                                                 // n in the low bits, which shift to the exponent
+  const uint64_t scale = f2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
+                            __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u));
+  return fma2(y, scale, acc);
 }
 
 // 16 consecutive head dims of a cached row as bf16 (two 16-byte chunks).
@@ -247,34 +280,46 @@ prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const CacheAttnPa
       uint64_t acc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = f2(0.f, 0.f);
-      const bool diagonal = p.causal && k0 + BK - 1 - off > q0;    // warp-uniform
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t x[32];
-        tmem_ld32(tS + 32 * ch, x);
+      auto tile = [&](auto diagonal) {
+        uint32_t xs[2][32];
+        tmem_ld32(tS, xs[0]);
         tmem_wait_ld();
-        if (ch == 3) {                                             // all of the tile is in registers
-          tc_fence_before();
-          mbar_arrive(bar(kBarSEmpty + buf));
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 e = lse[8 * ch + i];                        // minus lse; rows past q_len: -infinity, weight 0
-          const uint64_t y0 = fma2(f2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), c2, f2(e.x, e.y));
-          const uint64_t y1 =
-              fma2(f2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), c2, f2(e.z, e.w));
-          float v[4];
-          unf2(y0, v[0], v[1]);
-          unf2(y1, v[2], v[3]);
-          if (diagonal) {
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t (&x)[32] = xs[ch & 1];
+          if (ch < 3) tmem_ld32(tS + 32 * (ch + 1), xs[(ch + 1) & 1]);         // lands while this quarter is summed
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (32 * ch + 4 * i + b < first_col) v[b] = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const float4 e = lse[8 * ch + i];                      // minus lse; rows past q_len: -infinity, weight 0
+            const uint64_t y0 =
+                fma2(f2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), c2, f2(e.x, e.y));
+            const uint64_t y1 =
+                fma2(f2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), c2, f2(e.z, e.w));
+            if ((i == 1 || i == 5) && !decltype(diagonal)::value) {
+              acc[2 * (i & 1)] = exp2_pair_add(y0, acc[2 * (i & 1)]);
+              acc[2 * (i & 1) + 1] = exp2_pair_add(y1, acc[2 * (i & 1) + 1]);
+              continue;
+            }
+            float v[4];
+            unf2(y0, v[0], v[1]);
+            unf2(y1, v[2], v[3]);
+            if (decltype(diagonal)::value) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (32 * ch + 4 * i + b < first_col) v[b] = -INFINITY;
+            }
+            acc[2 * (i & 1)] = add2(acc[2 * (i & 1)], f2(ex2(v[0]), ex2(v[1])));
+            acc[2 * (i & 1) + 1] = add2(acc[2 * (i & 1) + 1], f2(ex2(v[2]), ex2(v[3])));
           }
-          acc[2 * (i & 1)] = add2(acc[2 * (i & 1)], f2(ex2(v[0]), ex2(v[1])));
-          acc[2 * (i & 1) + 1] = add2(acc[2 * (i & 1) + 1], f2(ex2(v[2]), ex2(v[3])));
+          if (ch < 3) tmem_wait_ld();
+          if (ch == 2) {                                           // all of the tile is in registers
+            tc_fence_before();
+            mbar_arrive(bar(kBarSEmpty + buf));
+          }
         }
-      }
+      };
+      if (p.causal && k0 + BK - 1 - off > q0) tile(std::true_type{});          // warp-uniform
+      else tile(std::false_type{});
       mbar_arrive(bar(kBarQEmpty + st));                           // lse read
       float lo, hi;
       unf2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), lo, hi);
