@@ -30,15 +30,31 @@ struct Workspace {
 // Rows of the log2-sums a (sequence, head) has: whole tiles of the weights kernel.
 size_t lse_rows(int q_len) { return ((size_t)q_len + 127) / 128 * 128; }
 
+// Whether a call's query rows go through the split kernel as so many heads (each
+// 16 rows of a kv head read its keys again, but the keys are split over CTAs) or
+// through the prefill kernel (whose tile of 128 rows of one head costs the same
+// however few are filled, and which walks all keys in one CTA).  Per 128 keys and
+// kv head the first takes about 2400 cycles of an SM for each 16 rows, the second
+// about 3000 for each head: even at some 16 rows a head, and at more where the
+// prefill's CTAs do not fill the 148 SMs.
+bool few_rows(int num_seqs, int q_len, int H, int H_kv, int max_seq_len, bool weights) {
+  if (q_len == 1) return true;
+  if ((long long)(H / H_kv) * q_len > 256 || (long long)H * q_len > 65535) return false;
+  // the scores of every row go through memory
+  if (weights && (long long)num_seqs * H * q_len * max_seq_len > (1LL << 27)) return false;
+  return q_len <= 16 || ((long long)q_len * num_seqs * H <= 16LL * 148 && max_seq_len >= 2048);
+}
+
 Workspace attn_workspace(int num_seqs, int q_len, int H, int H_kv, int max_seq_len, int page_size, bool weights) {
   Workspace w;
-  if (q_len == 1) {
+  if (few_rows(num_seqs, q_len, H, H_kv, max_seq_len, weights)) {
+    const int rows = H * q_len;
     int split = 0, nsplit = 0;
-    pkv::cache_decode_plan(num_seqs, H, H_kv, max_seq_len, page_size, &split, &nsplit);
-    const size_t per = (size_t)num_seqs * H * nsplit;
+    pkv::cache_decode_plan(num_seqs, rows, H_kv, max_seq_len, page_size, &split, &nsplit);
+    const size_t per = (size_t)num_seqs * rows * nsplit;
     if (nsplit > 1) w.o = per * 128 * sizeof(float);
     if (nsplit > 1 || weights) w.ml = per * sizeof(float2);
-    if (weights) w.logits = (size_t)num_seqs * H * max_seq_len * sizeof(float);
+    if (weights) w.logits = (size_t)num_seqs * rows * max_seq_len * sizeof(float);
   } else if (weights) {
     w.lse = (size_t)num_seqs * H * lse_rows(q_len) * sizeof(float);
   }
@@ -98,8 +114,9 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
   p.cache_dtype = cache_dtype, p.causal = causal;
   p.scale = scale, p.scale_log2 = scale * pkv::kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (q_len == 1) {
-    pkv::cache_decode_plan(num_seqs, H, H_kv, max_seq_len, page_size, &p.split_tokens, &p.max_splits);
+  if (few_rows(num_seqs, q_len, H, H_kv, max_seq_len, weights != nullptr)) {
+    p.H = H * q_len;
+    pkv::cache_decode_plan(num_seqs, p.H, H_kv, max_seq_len, page_size, &p.split_tokens, &p.max_splits);
     return pkv::cuda_status(pkv::launch_cache_decode(p, st));
   }
   pkv::PrefillParams f{};

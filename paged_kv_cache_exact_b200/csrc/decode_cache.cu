@@ -1,6 +1,8 @@
-// Single-token attention over a cache held in 8 bits, and single-token
-// attention (over an 8-bit or a bf16 cache) that also adds every key's softmax
-// weight to an accumulator.
+// Attention of single tokens, or of a few, over a cache held in 8 bits, and the
+// same (over an 8-bit or a bf16 cache) that also adds every key's softmax weight
+// to an accumulator.  Several query tokens are taken as more heads: the rows
+// [H, q_len] of a sequence lie one after the other, and row (h, i) differs from a
+// head of its own only in the last key it sees.
 //
 // What bounds it is reading the cache: 256 bytes (8-bit) or 512 bytes (bf16)
 // per token and kv head, plus 8 bytes of scales per block.  So every K/V row
@@ -149,6 +151,7 @@ cache_decode_kernel(const CacheAttnParams p) {
   const int hg0 = (blockIdx.x % n_hg) * kHeads;             // first head within the group
   const int h0 = kvh * group + hg0;
   const int nh = min(kHeads, group - hg0);
+  const int q_len = p.q_len;                                 // p.H counts rows: heads times q_len
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
 
@@ -163,7 +166,7 @@ cache_decode_kernel(const CacheAttnParams p) {
     mine_lp[i] = tid + i * kThreads < n_lp ? p.block_table[(size_t)s * p.max_pages + lp0 + tid + i * kThreads] : -1;
   int L = p.seq_lens[s];
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
-  if (L < 1 || L > cap) {
+  if (L < q_len || L > cap) {
     if (split == 0 && blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
     L = max(0, min(L, cap));
   }
@@ -288,6 +291,15 @@ cache_decode_kernel(const CacheAttnParams p) {
 #pragma unroll
   for (int i = 0; i < Lay::kStages - 1; ++i) prefetch_step(warp + i * kWarps * U, i);
 
+  int end[NT][2];                                            // keys before it are seen by column 2 t4 + j
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = (hg0 + 8 * nt + 2 * t4 + j) % q_len;
+      end[nt][j] = p.causal ? min(t_end, L - q_len + row + 1) : t_end;
+    }
+
   float o[NT][8][4];
   float m[NT][2], l[NT][2];
 #pragma unroll
@@ -368,15 +380,15 @@ cache_decode_kernel(const CacheAttnParams p) {
     bool passed = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in0 = page_ok[u] && tok[u] + g < t_end, in1 = page_ok[u] && tok[u] + g + 8 < t_end;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float (&x)[4] = sc[u][nt];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const float f = hm[nt][j] * scales[u].x;
-          x[j] = in0 ? (x[j] + sd[u][nt][j]) * f : -INFINITY;
-          x[2 + j] = in1 ? (x[2 + j] + sd[u][nt][2 + j]) * f : -INFINITY;
+          const int left = page_ok[u] ? end[nt][j] - tok[u] : 0;         // visible tokens of the chunk
+          x[j] = g < left ? (x[j] + sd[u][nt][j]) * f : -INFINITY;
+          x[2 + j] = g + 8 < left ? (x[2 + j] + sd[u][nt][2 + j]) * f : -INFINITY;
           passed = passed || fmaxf(x[j], x[2 + j]) > m[nt][j] + (Lay::kLift + 8.f);
         }
       }
@@ -581,41 +593,65 @@ PKV_DEVINLINE void merge_rows(const CacheAttnParams& p, long long sh) {
   out[1] = __floats2bfloat162_rn(none ? 0.f : acc.z / lsum, none ? 0.f : acc.w / lsum);
 }
 
-// Scores -> weights, for a range of a sequence's tokens and a kv head.  Each thread
-// owns tokens; a token's weight is the sum over the group's heads of 2^(x - lse).
+// Scores -> weights, for a range of a sequence's tokens and a kv head.  p.token_lanes
+// lanes share a token's scores (32 of them where a kv head has that many rows) and
+// their sums are added up in one order; a token's weight is the sum over the
+// group's rows of 2^(x - lse).
 constexpr int kWeightThreads = 256;
-constexpr int kWeightTokens = 1024;               // tokens a CTA
-constexpr int kMaxGroup = 256;                    // query heads per kv head
+constexpr int kMaxGroup = 256;                    // query rows per kv head
 PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, int s) {
-  __shared__ float s_lse[kMaxGroup];
+  __shared__ __align__(16) float s_lse[kMaxGroup];
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
   const int L = max(0, min(p.seq_lens[s], cap));
-  const int t0 = range * kWeightTokens;
+  const int t0 = range * p.range_tokens;
   if (t0 >= L) return;
   const int group = p.H / p.H_kv;
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
-  for (int h = threadIdx.x >> 5; h < group; h += kWeightThreads / 32) {
-    float M, lsum;
-    merge_ml(p.ws_ml + ((size_t)s * p.H + kvh * group + h) * p.max_splits, nsplit, threadIdx.x & 31, M, lsum);
-    // no visible key: every score is -inf, and 2^(-inf - 0) = 0
-    if ((threadIdx.x & 31) == 0) s_lse[h] = lsum == 0.f ? 0.f : M + log2f(lsum);
+  const float2* ml = p.ws_ml + ((size_t)s * p.H + kvh * group) * p.max_splits;
+  // no visible key: every score is -inf, and 2^(-inf - 0) = 0
+  if (group <= kWeightThreads / 32) {             // a warp a row
+    const int h = threadIdx.x >> 5;
+    if (h < group) {
+      float M, lsum;
+      merge_ml(ml + (size_t)h * p.max_splits, nsplit, threadIdx.x & 31, M, lsum);
+      if ((threadIdx.x & 31) == 0) s_lse[h] = lsum == 0.f ? 0.f : M + log2f(lsum);
+    }
+  } else if (threadIdx.x < group) {               // a thread a row
+    const float2* row = ml + (size_t)threadIdx.x * p.max_splits;
+    float M = -INFINITY, lsum = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < nsplit; ++j) M = fmaxf(M, row[j].x);
+#pragma unroll 8
+    for (int j = 0; j < nsplit; ++j) {
+      const float2 v = row[j];
+      lsum = fmaf(v.x == -INFINITY && M == -INFINITY ? 1.f : ex2(v.x - M), v.y, lsum);
+    }
+    s_lse[threadIdx.x] = lsum == 0.f ? 0.f : M + log2f(lsum);
   }
   __syncthreads();
   const size_t sk = (size_t)s * p.H_kv + kvh;
   const float* lg = p.logits + sk * p.logit_tokens * group;
   float* w = p.weights + sk * p.weights_stride;
-  for (int t = t0 + threadIdx.x; t < min(L, t0 + kWeightTokens); t += kWeightThreads) {
-    const float* x = lg + (size_t)t * group;
+  const int lanes = p.token_lanes, mine = threadIdx.x % lanes;
+  const int t_end = min(L, t0 + p.range_tokens);
+  for (int t1 = t0; t1 < t_end; t1 += kWeightThreads / lanes) {              // a warp's trip count is uniform
+    const int t = t1 + threadIdx.x / lanes;
     float sum = 0.f;
-    if ((group & 3) == 0) {
-      for (int h = 0; h < group; h += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(x + h);
-        sum += (ex2(v.x - s_lse[h]) + ex2(v.y - s_lse[h + 1])) + (ex2(v.z - s_lse[h + 2]) + ex2(v.w - s_lse[h + 3]));
+    if (t < t_end) {
+      const float* x = lg + (size_t)t * group;
+      if ((group & 3) == 0) {
+#pragma unroll 2
+        for (int h = 4 * mine; h < group; h += 4 * lanes) {
+          const float4 v = *reinterpret_cast<const float4*>(x + h);
+          const float4 e = *reinterpret_cast<const float4*>(s_lse + h);
+          sum += (ex2(v.x - e.x) + ex2(v.y - e.y)) + (ex2(v.z - e.z) + ex2(v.w - e.w));
+        }
+      } else {
+        for (int h = mine; h < group; h += lanes) sum += ex2(x[h] - s_lse[h]);
       }
-    } else {
-      for (int h = 0; h < group; ++h) sum += ex2(x[h] - s_lse[h]);
     }
-    w[t] += sum;
+    for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (t < t_end && mine == 0) w[t] += sum;
   }
 }
 
@@ -628,7 +664,7 @@ __global__ void __launch_bounds__(kWeightThreads) cache_finish_kernel(const Cach
     merge_rows(p, (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5));
     return;
   }
-  const int ranges = (p.max_seq_len + kWeightTokens - 1) / kWeightTokens;
+  const int ranges = (p.max_seq_len + p.range_tokens - 1) / p.range_tokens;
   const int i = blockIdx.x - p.merge_ctas;
   const int pair = i / ranges;
   range_weights(p, i - pair * ranges, pair % p.H_kv, pair / p.H_kv);
@@ -718,7 +754,13 @@ cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
   q.merge_ctas = 0;
   if (p.max_splits > 1) q.merge_ctas = (int)(((long long)p.num_seqs * p.H + kMergeWarps - 1) / kMergeWarps);
   long long ctas = q.merge_ctas;
-  if (w) ctas += (long long)((p.max_seq_len + kWeightTokens - 1) / kWeightTokens) * p.H_kv * p.num_seqs;
+  if (w) {
+    const int group = p.H / p.H_kv;
+    q.token_lanes = 1;                              // at most 8 scores a lane, while lanes last
+    while (q.token_lanes < 32 && q.token_lanes * 8 < group) q.token_lanes *= 2;
+    q.range_tokens = q.token_lanes > 8 ? 128 : 1024 / q.token_lanes;
+    ctas += (((long long)p.max_seq_len + q.range_tokens - 1) / q.range_tokens) * p.H_kv * p.num_seqs;
+  }
   if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;
   return ctas ? launch_after(cache_finish_kernel, dim3((unsigned)ctas), kWeightThreads, q, stream) : cudaSuccess;
 }

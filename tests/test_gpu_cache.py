@@ -108,7 +108,7 @@ class Cache:
         want, ww, spread, size = attend(self.q, self.k, self.v, self.ks, self.vs, self.table, lens, causal, self.scale)
         e = 128 * 2.0 ** -24 * size
         rel = math.expm1(2 * e) + 2.0 ** -20
-        # P is rounded to bf16 for a bf16 cache and in the prefill kernel, else to f16
+        # P is rounded to bf16 for a bf16 cache and in the prefill kernel (many rows), else to f16
         p_round = 2.0 ** -8 if self.dtype == BF16 or self.q.shape[2] > 1 else 2.0 ** -11
         tol = 2.0 ** -8 * want.abs() + (p_round + rel) * 1.01 * spread + 1e-30
         err = (out.double() - want).abs()
@@ -334,13 +334,47 @@ def test_many_query_rows(dtype, case, causal):
     before = c.w.clone()
     out = c.run(True, causal=causal, max_len=max(lens) + 3)
     c.check(out, before, causal=causal)
-    if dtype == BF16:           # the same kernel as without weights, to the bit
+    if dtype == BF16 and q_len >= 257:      # the same kernel as without weights, to the bit
         plain = api.paged(c.q, c.k, c.v, c.table, c.len_t, ps, causal, c.scale, max(lens))
         assert torch.equal(plain, out)
     w = c.w.clone()
     c.w = before.clone()
     c.run(True, causal=causal, max_len=max(lens) + 3)
     assert torch.equal(c.w, w)
+
+
+FEW = [
+    # a few query rows a head, as many as a verifying step has: q_len, lens, H, H_kv, page, block
+    (2, [700, 2, 3, 4100], 8, 8, 16, 16),
+    (3, [3, 257, 1030], 15, 3, 32, 32),
+    (5, [5, 6, 2600, 64], 16, 2, 64, 16),
+    (16, [16, 17, 900], 32, 2, 256, 64),          # 256 rows a kv head
+    (17, [2500], 4, 4, 16, 16),
+    (60, [6000], 8, 2, 128, 32),
+    (61, [400, 61], 4, 1, 16, 16),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("case", range(len(FEW)))
+def test_few_query_rows(dtype, case, causal):
+    q_len, lens, H, H_kv, ps, bt = FEW[case]
+    c = Cache(dtype, lens, H, H_kv, ps, bt, q_len=q_len, seed=40 + case, q_mul=2.0)
+    if dtype != BF16:
+        c.check(c.run(False, causal=causal), causal=causal)
+    before = c.w.clone()
+    c.check(c.run(True, causal=causal, max_len=max(lens) + 3), before, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+def test_few_query_rows_more_than_keys(dtype):
+    c = Cache(dtype, [4, 9, 200], 4, 2, 16, 16, q_len=9, seed=50)
+    before = c.w.clone()
+    out = c.run(True)
+    assert clean() == B.PKV_DEVERR_BAD_LEN
+    c.check(out, before)
+    assert (out[0, :, :5] == 0).all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
