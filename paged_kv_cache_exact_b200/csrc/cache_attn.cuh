@@ -50,7 +50,7 @@ struct CacheAttnParams {
   unsigned int* err;
   int num_seqs, q_len, H, H_kv, page_size, page_shift, block_shift, num_pages, max_pages, max_seq_len;
   int split_tokens, max_splits, weights_stride, logit_tokens, lse_stride;
-  int merge_ctas, token_lanes, range_tokens;   // set by the launcher
+  int merge_ctas, merge_warps, token_lanes, range_tokens;   // set by the launcher
   int cache_dtype, causal;
   float scale, scale_log2;     // scale_log2 = scale * log2(e)
 };

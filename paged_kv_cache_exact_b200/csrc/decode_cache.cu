@@ -563,29 +563,46 @@ PKV_DEVINLINE void merge_ml(const float2* ml, int nsplit, int lane, float& M, fl
   for (int o = 16; o; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
 }
 
-// Splits -> output: one warp per (sequence, head), lane i owns head dims 4i .. 4i+3.
+// Splits -> output: p.merge_warps warps per (sequence, head) take its splits in
+// turn (one warp walks 30 splits in 8 dependent rounds of loads); lane i owns head
+// dims 4i .. 4i+3.
 constexpr int kMergeWarps = 8;
-PKV_DEVINLINE void merge_rows(const CacheAttnParams& p, long long sh) {
-  const int lane = threadIdx.x & 31;
-  if (sh >= (long long)p.num_seqs * p.H) return;
+PKV_DEVINLINE void merge_rows(const CacheAttnParams& p, int cta) {
+  __shared__ float4 s_acc[kMergeWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mw = p.merge_warps, part = warp % mw;
+  const long long sh = (long long)cta * (kMergeWarps / mw) + warp / mw;
   const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
-  const int L = max(0, min(p.seq_lens[sh / p.H], cap));
+  const bool row = sh < (long long)p.num_seqs * p.H;
+  const int L = row ? max(0, min(p.seq_lens[sh / p.H], cap)) : 0;
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
-  if (nsplit <= 1) return;
-  const float2* ml = p.ws_ml + sh * p.max_splits;
-  float M, lsum;
-  merge_ml(ml, nsplit, lane, M, lsum);
-  const float4* po = reinterpret_cast<const float4*>(p.ws_o + sh * p.max_splits * D) + lane;
+  const bool live = nsplit > 1;                     // one split: written by the split kernel
+  float M = -INFINITY, lsum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    const float2* ml = p.ws_ml + sh * p.max_splits;
+    merge_ml(ml, nsplit, lane, M, lsum);
+    const float4* po = reinterpret_cast<const float4*>(p.ws_o + sh * p.max_splits * D) + lane;
 #pragma unroll 4
-  for (int j = 0; j < nsplit; ++j) {
-    const float mj = ml[j].x;
-    const float w = mj == -INFINITY && M == -INFINITY ? 1.f : ex2(mj - M);
-    const float4 x = po[(size_t)j * (D / 4)];
-    acc.x = fmaf(w, x.x, acc.x);
-    acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z);
-    acc.w = fmaf(w, x.w, acc.w);
+    for (int j = part; j < nsplit; j += mw) {
+      const float mj = ml[j].x;
+      const float w = mj == -INFINITY && M == -INFINITY ? 1.f : ex2(mj - M);
+      const float4 x = po[(size_t)j * (D / 4)];
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+  }
+  s_acc[warp][lane] = acc;
+  __syncthreads();
+  if (!live || part) return;
+  for (int i = 1; i < mw; ++i) {
+    const float4 x = s_acc[warp + i][lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
   }
   const bool none = lsum == 0.f;
   __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(p.out + sh * D) + 2 * lane;
@@ -656,12 +673,12 @@ PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, i
 }
 
 // What follows the split kernel, in one launch: the first p.merge_ctas CTAs merge
-// splits, a warp a (sequence, head); the others take the weights' ranges.
+// splits; the others take the weights' ranges.
 static_assert(kMergeWarps * 32 == kWeightThreads, "one block size");
 __global__ void __launch_bounds__(kWeightThreads) cache_finish_kernel(const CacheAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if ((int)blockIdx.x < p.merge_ctas) {
-    merge_rows(p, (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5));
+    merge_rows(p, blockIdx.x);
     return;
   }
   const int ranges = (p.max_seq_len + p.range_tokens - 1) / p.range_tokens;
@@ -725,16 +742,22 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
   const int group = H / H_kv;
   const int heads = group > 8 ? 16 : 8;
   const long long pairs = (long long)num_seqs * H_kv * ((group + heads - 1) / heads);
-  int st = 64 < page_size ? page_size : 64;
+  // At least what the four warps work on at once: two chunks of 16 tokens each.
+  const int unit = 128 < page_size ? page_size : 128;
+  int st = unit;
   // Short contexts: one split, as the merge's launch costs more than the splits
-  // save (one sequence of 437 tokens, 8 kv heads: 10.4 us in 7 splits).
+  // save (one sequence of 437 tokens, 8 kv heads: 10.4 us in 7 splits, 8.3 in one).
   if (max_seq_len <= kOneSplit) st = kOneSplit;
+  // Little work: as many splits as run at once, three CTAs an SM (one sequence of
+  // 32000 tokens, 8 kv heads: 41 us in 128-token splits, four turns and a half; 23 in one).
+  const long long turn = (pairs * max_seq_len + 148 * 3 - 1) / (148 * 3);
+  if (st < turn && turn <= 1024) st = (int)((turn + unit - 1) / unit * unit);
   // Double while at least 8 CTAs per SM remain.  A split writes (and the merge
   // reads) 512 bytes per query head: with few heads that is little, and shorter
   // splits balance ragged lengths better (64 sequences x 32 heads, int8: 441 us at
   // 1024 tokens, 455 at 4096; 16 long ones x 8 heads a kv head: 141 and 137 us).
   const int most = group >= 4 ? kMaxSplitTokens : 1024;
-  while (st < most && pairs * ((max_seq_len + 2LL * st - 1) / (2LL * st)) >= 148LL * 8) st *= 2;
+  while (turn > 1024 && st < most && pairs * ((max_seq_len + 2LL * st - 1) / (2LL * st)) >= 148LL * 8) st *= 2;
   while (((long long)max_seq_len + st - 1) / st > kMaxSplits && st < kMaxSplitTokens) st *= 2;
   *split_tokens = st;
   *max_splits = (int)(((long long)max_seq_len + st - 1) / st);
@@ -752,7 +775,14 @@ cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   CacheAttnParams q = p;
   q.merge_ctas = 0;
-  if (p.max_splits > 1) q.merge_ctas = (int)(((long long)p.num_seqs * p.H + kMergeWarps - 1) / kMergeWarps);
+  if (p.max_splits > 1) {
+    q.merge_warps = 1;                              // about four splits a warp
+    while (q.merge_warps < kMergeWarps && q.merge_warps * 4 < p.max_splits) q.merge_warps *= 2;
+    const int rows = kMergeWarps / q.merge_warps;
+    const long long n = ((long long)p.num_seqs * p.H + rows - 1) / rows;
+    if (n > 0x3fffffffLL) return cudaErrorNotSupported;
+    q.merge_ctas = (int)n;
+  }
   long long ctas = q.merge_ctas;
   if (w) {
     const int group = p.H / p.H_kv;
