@@ -365,8 +365,13 @@ PKV_API int paged_kv_copy_pages_q8(void* k_pages, void* v_pages, void* k_scales,
  * What paged_attn computes with K and V the values the codes stand for; q and
  * out are PKV_BF16.  Arguments that both have mean the same (the page table, the
  * lengths, q_len == 1 for decode, causal, the rules for bad pages and lengths).
+ * A few query rows (what a verifying step has: q_len up to 16, and more where
+ * that leaves most of the GPU idle) run on the split kernel of the single-token
+ * case, more of them on the prefill kernel; the choice depends on the sizes alone.
  * workspace : device scratch of >= paged_attn_q8_workspace_size() bytes, 256-byte
  *             aligned (NULL if that size is 0), one for each call in flight.
+ * Codes of live tokens are finite: an e4m3 NaN code (0x7f, 0xff) never comes from
+ * paged_kv_append_q8, and what attention makes of one is not defined.
  */
 PKV_API size_t paged_attn_q8_workspace_size(int num_seqs, int q_len, int H, int H_kv,
                                             int max_seq_len, int page_size);
@@ -397,7 +402,8 @@ PKV_API int paged_attn_q8(const void* q, const void* k_pages, const void* v_page
  *
  * k_scales, v_scales, block_tokens : as in paged_attn_q8; not looked at when
  *             cache_dtype is PKV_BF16.
- * weights   : device float32 [num_seqs, H_kv, weights_stride], added to.
+ * weights   : device float32 [num_seqs, H_kv, weights_stride], added to.  Two calls
+ *             in flight must not share it.
  * weights_stride : >= max_seq_len.
  * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.
  * H / H_kv is at most 256.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
@@ -436,7 +442,7 @@ PKV_API int paged_attn_weights(const void* q, const void* k_pages, const void* v
  * seq_lens    : lengths before; new_lens: lengths after (another array).
  * kept        : device int32 [num_seqs, H_kv, budget]: the kept tokens' old
  *               indices, ascending, -1 from m on.
- * budget      : >= 1; recent: in [0, budget].
+ * budget      : in [1, 2^30]; recent: in [0, budget].
  * cache_dtype : PKV_BF16 or PKV_F32 (d 64 or 128; k_scales, v_scales and
  *               block_tokens are not looked at), PKV_I8 or PKV_E4M3 (d 128).
  *               An 8-bit block's new scale is the largest of its rows' scales,

@@ -121,8 +121,10 @@ def _int32(*tensors):
 
 
 def _workspace(workspace, n, device):
-    if workspace is None and n:
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor of the same device")
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 

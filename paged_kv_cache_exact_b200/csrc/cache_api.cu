@@ -245,7 +245,7 @@ int paged_kv_evict(void* k_pages, void* v_pages, void* k_scales, void* v_scales,
       (long long)max_pages_per_seq * page_size < max_seq_len)
     return PKV_ERR_INVALID_ARG;
   if (q8 ? d != 128 : (d != 64 && d != 128)) return PKV_ERR_UNSUPPORTED;
-  if (num_seqs > 65535 || H_kv > 65535 || (long long)num_pages * page_size > (1LL << 31))
+  if (num_seqs > 65535 || H_kv > 65535 || budget > (1 << 30) || (long long)num_pages * page_size > (1LL << 31))
     return PKV_ERR_UNSUPPORTED;
   const size_t need = paged_kv_evict_workspace_size(num_seqs, H_kv, budget, block_tokens, cache_dtype);
   if (need > 0 && (!aligned(workspace, 256) || workspace_bytes < need)) return PKV_ERR_WORKSPACE;

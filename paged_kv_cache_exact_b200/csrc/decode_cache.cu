@@ -764,6 +764,7 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
 }
 
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
+  if (p.max_splits > 65535) return cudaErrorNotSupported;           // sequences beyond 2^28 tokens
   const bool w = p.weights != nullptr;
   cudaError_t e;
   if (p.cache_dtype == PKV_I8)

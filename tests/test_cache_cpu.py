@@ -97,7 +97,7 @@ EVICT_OK = [FAKE] * 6 + [2000] + [FAKE, FAKE, FAKE, FAKE + 64, FAKE] + [100, 10,
     (dict(ks=None), INV), (dict(bt=64), INV), (dict(budget=0), INV), (dict(recent=-1), INV), (dict(recent=101), INV),
     (dict(S=0), INV), (dict(H_kv=0), INV), (dict(P=0), INV), (dict(ps=20), INV), (dict(maxp=3), INV),
     (dict(max_len=0), INV), (dict(stride=1999), INV), (dict(cache=9), INV),
-    (dict(d=64), UNSUP), (dict(d=96, cache=B.PKV_BF16), UNSUP), (dict(S=70000), UNSUP), (dict(P=1 << 28), UNSUP),
+    (dict(d=64), UNSUP), (dict(budget=(1 << 30) + 1), UNSUP), (dict(d=96, cache=B.PKV_BF16), UNSUP), (dict(S=70000), UNSUP), (dict(P=1 << 28), UNSUP),
     (dict(ws=None), WS), (dict(ws=FAKE + 8), WS), (dict(ws_bytes=100), WS),
 ])
 def test_evict_rejects_bad_arguments(kw, status):
