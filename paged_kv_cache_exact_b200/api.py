@@ -17,6 +17,7 @@ another stream the caller orders against the tensors' producers and consumers
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -99,20 +100,20 @@ def _stream_of(stream, t):
 
 def _pools(k_pages, v_pages, k_scales, v_scales):
     """(cache dtype, tokens a block) of a pool of pages and its scales."""
-    _need(k_pages.dim() == 4 and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
+    shape, dtype = k_pages.shape, k_pages.dtype
+    _need(len(shape) == 4 and v_pages.shape == shape and v_pages.dtype == dtype,
           "k_pages and v_pages must be [pages, page_size, H_kv, d] of one type")
-    if k_pages.dtype in _DT:
+    if dtype in _DT:
         _need(k_scales is None and v_scales is None, "only an 8-bit cache has scales")
-        return _DT[k_pages.dtype], 0
-    if k_pages.dtype not in _Q8:
-        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+        return _DT[dtype], 0
+    if dtype not in _Q8:
+        raise TypeError(f"unsupported cache dtype {dtype}")
     _need(k_scales is not None and v_scales is not None, "an 8-bit cache needs its scales")
-    P, ps, H_kv, _ = k_pages.shape
     _need(k_scales.dtype == torch.float32 and v_scales.dtype == torch.float32, "scales must be float32")
-    _need(k_scales.dim() == 3 and v_scales.shape == k_scales.shape and k_scales.shape[0] == P
-          and k_scales.shape[2] == H_kv and k_scales.shape[1] > 0 and ps % k_scales.shape[1] == 0,
-          "scales must be [pages, page_size / block_tokens, H_kv]")
-    return _Q8[k_pages.dtype], ps // k_scales.shape[1]
+    blocks = k_scales.shape
+    _need(len(blocks) == 3 and v_scales.shape == blocks and blocks[0] == shape[0] and blocks[2] == shape[2]
+          and blocks[1] > 0 and shape[1] % blocks[1] == 0, "scales must be [pages, page_size / block_tokens, H_kv]")
+    return _Q8[dtype], shape[1] // blocks[1]
 
 
 def _int32(*tensors):
@@ -135,6 +136,12 @@ def _used_on(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(st)
+
+
+# Sizes alone decide a workspace's bytes.
+_q8_bytes = functools.lru_cache(4096)(B.paged_attn_q8_workspace_size)
+_weights_bytes = functools.lru_cache(4096)(B.paged_attn_weights_workspace_size)
+_evict_bytes = functools.lru_cache(4096)(B.paged_kv_evict_workspace_size)
 
 
 def append_q8(k_new, v_new, cu_new, start_pos, block_table, k_pages, v_pages, k_scales, v_scales,
@@ -190,7 +197,7 @@ def paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, pag
         raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
     S, H, q_len, d, H_kv, o = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
     with _on_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, o):
-        ws, n = _workspace(workspace, B.paged_attn_q8_workspace_size(S, q_len, H, H_kv, max_seq_len, page_size),
+        ws, n = _workspace(workspace, _q8_bytes(S, q_len, H, H_kv, max_seq_len, page_size),
                            q.device)
         B.paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S, q_len,
                         H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale, cache, o,
@@ -210,7 +217,7 @@ def paged_weights(q, k_pages, v_pages, block_table, seq_lens, page_size: int, ca
           and weights.shape[2] >= max_seq_len, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
     more = () if block == 0 else (k_scales, v_scales)
     with _on_device(q, k_pages, v_pages, block_table, seq_lens, o, weights, *more):
-        ws, n = _workspace(workspace, B.paged_attn_weights_workspace_size(S, q_len, H, H_kv, max_seq_len, page_size),
+        ws, n = _workspace(workspace, _weights_bytes(S, q_len, H, H_kv, max_seq_len, page_size),
                            q.device)
         B.paged_attn_weights(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S,
                              q_len, H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale,
@@ -239,9 +246,9 @@ def evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, recent:
           and weights_out.dtype == torch.float32, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
     more = () if block == 0 else (k_scales, v_scales)
     with _on_device(k_pages, v_pages, weights, weights_out, block_table, dst_table, seq_lens, *more):
-        kept = torch.empty((S, H_kv, max(budget, 0)), dtype=torch.int32, device=k_pages.device)
+        kept = seq_lens.new_empty((S, H_kv, max(budget, 0)))
         new_lens = torch.empty_like(seq_lens)
-        ws, n = _workspace(workspace, B.paged_kv_evict_workspace_size(S, H_kv, budget, block, cache), k_pages.device)
+        ws, n = _workspace(workspace, _evict_bytes(S, H_kv, budget, block, cache), k_pages.device)
         B.paged_kv_evict(k_pages, v_pages, k_scales, v_scales, weights, weights_out, weights.shape[2], block_table,
                          dst_table, seq_lens, new_lens, kept, budget, recent, S, H_kv, d, P, ps, block,
                          block_table.shape[1], max_seq_len, cache, ws, n, _stream_of(stream, k_pages))
