@@ -6,9 +6,10 @@
 //
 // What bounds it is reading the cache: 256 bytes (8-bit) or 512 bytes (bf16)
 // per token and kv head, plus 8 bytes of scales per block.  So every K/V row
-// is read once for all query heads of its kv head, straight from HBM into the
-// registers that feed the tensor cores: there is no shared-memory staging, and
-// a warp always has one chunk of 16 tokens in flight while it works on another.
+// is read once for all query heads of its kv head.  Each of a CTA's four warps
+// takes chunks of 16 tokens of its own (two at a time of an 8-bit cache) through a
+// two-step cp.async ring: 8 KB a warp and 96 KB an SM are on their way while as
+// much is worked on, and no barrier joins the warps before the end.
 //
 // Products.  With up to 8 query heads per kv head (16 in two tiles) scores and
 // outputs are small matrix products, written transposed so that the long axis
@@ -17,7 +18,8 @@
 // both mma.sync m16n8k16; tcgen05's smallest tile (M = 64 in TMEM) would be
 // three quarters padding, and the tensor pipe is far from the bound here.
 // The index that a product sums over may be permuted freely and so may the rows
-// of O^T, which is what lets each lane take 16 consecutive bytes of a row:
+// of O^T, which is what lets each lane read 16 consecutive bytes of a row from the
+// ring:
 //   K: lane (g, t) = (lane / 4, lane % 4) reads rows g and g + 8;
 //   V: lane (g, t) reads rows 2t, 2t+1, 2t+8, 2t+9 at bytes 16 g, and pairs of
 //      rows are interleaved in registers (prmt), which transposes V.
@@ -27,9 +29,9 @@
 // Numbers.  Codes of both formats are exact in f16, so products run on f16
 // codes: q is scaled by a power of two per head so that its largest element
 // lies in [2^14, 2^15) (f16 keeps 11 bits, bf16 has 8: exact but for elements
-// below 2^-24 of the largest, whose error is under 2^-39 of it).  P is rounded to f16, lifted by 2^7 against
-// the reference maximum so that weights down to 2^-21 of the largest keep all
-// 11 bits and those below 2^-32 of it vanish.  A bf16 cache runs on bf16
+// below 2^-24 of the largest, whose error is under 2^-39 of it).  P is rounded to
+// f16, lifted by 2^7 against the reference maximum so that weights down to 2^-21
+// of the largest keep all 11 bits and those below 2^-32 of it vanish.  A bf16 cache runs on bf16
 // products and P in bf16, as in the other decode kernels.  Scales are applied
 // in float32: ks to the score, vs to each chunk's P V product (a chunk of 16
 // tokens lies in one block).  Sums and maxima are float32; the reference
@@ -37,8 +39,8 @@
 //
 // Weights need the row's final maximum and sum, so the scores (float32, base-2
 // units) go to the workspace and a second kernel turns them into weights once
-// the splits are merged: each (sequence, kv head, token) is owned by one
-// thread, so there are no atomics and the sums have one order.
+// the splits are merged: each (sequence, kv head, token) has its own lanes, so
+// there are no atomics and the sums have one order.
 #include <mutex>
 
 #include "cache_attn.cuh"
@@ -138,7 +140,7 @@ cache_decode_kernel(const CacheAttnParams p) {
   constexpr int kHeads = 8 * NT;
   constexpr int U = Lay::kUnroll;
   constexpr int J = kOne ? 1 : 2;                            // columns of a lane
-  extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][piece][lane] 16 bytes
+  extern __shared__ __align__(16) uint8_t ring[];            // [warp][stage][chunk][K, V][row]
   __shared__ int s_pages[kMaxSplitPages];
   __shared__ __align__(8) float s_scale[kWarps][Lay::kStages][U][2];      // (ks, vs) of the chunks in the ring
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
@@ -349,6 +351,9 @@ cache_decode_kernel(const CacheAttnParams p) {
       tok[u] = t_begin + 16 * cu;
       page_ok[u] = cu < n_chunks && s_pages[(tok[u] >> p.page_shift) - lp0] >= 0;
       scales[u] = kBf16 ? make_float2(1.f, 1.f) : *reinterpret_cast<const float2*>(s_scale[warp][now][u]);
+      // A NaN value scale makes every row that sees the block NaN; said through the
+      // key scale, which masking keeps from rows that do not see it.
+      if (!kBf16 && isnan(scales[u].y)) scales[u] = make_float2(scales[u].y, 1.f);
     }
     // S^T = K Q^T, in two chains of four steps
     float sc[U][NT][4], sd[U][NT][4];

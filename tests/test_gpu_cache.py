@@ -412,6 +412,19 @@ def test_many_query_rows_leave_out_bad_pages(dtype, ps):
 
 @pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
 @pytest.mark.parametrize("which", ["ks", "vs"])
+def test_nan_behind_the_causal_mask_of_a_few_rows(dtype, which):
+    """The same for 12 rows of 100 keys: the block of keys 96 .. 99 is seen from row 8 on."""
+    c = Cache(dtype, [100, 70], 4, 2, 16, 16, q_len=12, seed=24)
+    getattr(c, which)[int(c.table[0, 6]), 0, 1] = float("nan")
+    out = c.run(True)
+    assert torch.isfinite(out[1]).all() and torch.isfinite(out[0, :2]).all()
+    assert torch.isfinite(out[0, 2:, :8]).all() and torch.isnan(out[0, 2:, 8:]).all()
+    assert torch.isfinite(c.w[1, :, :70]).all() and torch.isfinite(c.w[0, 0, :100]).all()
+    assert torch.isnan(c.w[0, 1, :100]).all()
+
+
+@pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
+@pytest.mark.parametrize("which", ["ks", "vs"])
 def test_nan_behind_the_causal_mask_stays_there(dtype, which):
     """A block whose scale is NaN reaches the rows that see it and no others, within one tile."""
     c = Cache(dtype, [100], 2, 1, 16, 16, q_len=100, seed=22)
