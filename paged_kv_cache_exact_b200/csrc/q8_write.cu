@@ -17,11 +17,13 @@
 // One CTA per (block of the call, a few of the 2 H_kv (head, K or V) pairs): a warp
 // takes 16 of a pair's rows, so a 16-token block has 8 pairs a CTA and a 128-token
 // block one.  Lane i holds elements 4i .. 4i+3 of a row, so a row of new values is
-// one 256-byte load and its codes one 128-byte store.  The rows stay in registers
-// between the maximum and the rounding (in a 256-token block a warp has 32 rows
-// and reads the second 16 again, from L2).  The bound is HBM: 2 bytes read and 1
-// written per element; the chain table -> rows -> scale -> codes is hidden by the
-// other CTAs of the SM.
+// one 256-byte load and its codes one 128-byte store.  The rows are read twice,
+// the second time from L1, four at a time: with 16 in registers the rounding is 16
+// copies of its code, which cost a decode step's single row 2 us of instruction
+// fetches (6.2 against 4.2 us) and gained a prompt nothing.  What bounds a prompt
+// is the rounding's instructions, 29 a code on 61% of the issue slots (78 us for
+// 30027 rows of 8 heads); the floor of 2 bytes read and 1 written per element is
+// 28 us.
 #include "cache_attn.cuh"
 #include "q8.cuh"
 
@@ -31,7 +33,8 @@ namespace {
 constexpr int D = 128;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHeld = 16;            // rows a warp takes
+constexpr int kWarpRows = 16;        // rows of a block that a warp takes
+constexpr int kBatch = 4;            // rows it loads at once
 
 // Four consecutive elements of a new row as stored (bf16 or f32).
 template <typename T> struct Row4;
@@ -67,7 +70,7 @@ template <> struct Row4<float> {
 // items from cu_new[s] / block + 2 s on, which leaves room for every block its
 // rows can touch: n rows touch at most floor(n / block) + 2 blocks.
 template <int kCache, typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_kernel(const AppendQ8Params p) {
+__global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const AppendQ8Params p) {
   __shared__ int s_row0, s_rows, s_off, s_dst;
   __shared__ uint32_t s_max[kWarps];
   if (threadIdx.x == 0) s_rows = 0;
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_ke
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bt = 1 << p.block_shift;
-  const int parts = min(kWarps, bt / kHeld);                       // warps a pair
+  const int parts = min(kWarps, bt / kWarpRows);                       // warps a pair
   const int pair = blockIdx.y * (kWarps / parts) + warp / parts;
   const int part = warp % parts;
   const bool live = pair < 2 * p.H_kv;
@@ -131,19 +134,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_ke
     const size_t code_stride = (size_t)p.H_kv * D / 4;              // words between tokens
 
     uint32_t m = 0;
-    Row4<T> x[kHeld];
+    Row4<T> x[kBatch];
+    auto load = [&](int r0) {                                       // rows r0, r0 + parts, ...: all before any is used
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {                               // rows part, part + parts, ...
-      const int r = part + i * parts;
-      if (live && r < rows) x[i].load(src, src_row + (size_t)r * p.H_kv, lane);
-    }
+      for (int i = 0; i < kBatch; ++i)
+        if (r0 + i * parts < rows) x[i].load(src, src_row + (size_t)(r0 + i * parts) * p.H_kv, lane);
+    };
+    if (live) {
+#pragma unroll 1
+      for (int r0 = part; r0 < rows; r0 += kBatch * parts) {
+        load(r0);
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (live && part + i * parts < rows) m = max(m, x[i].amax());
-#pragma unroll 8
-    for (int r = part + kHeld * parts; r < rows; r += parts) {
-      Row4<T> y;
-      if (live) y.load(src, src_row + (size_t)r * p.H_kv, lane), m = max(m, y.amax());
+        for (int i = 0; i < kBatch; ++i)
+          if (r0 + i * parts < rows) m = max(m, x[i].amax());
+      }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (parts > 1) {
@@ -177,14 +181,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) append_q8_ke
       const uint32_t w = codes_of4<kCache>(q, [&](int i, float h) { return fmaf(-h, den, v[i]); });
       code[(size_t)(off + r) * code_stride] = broken ? 0u : w;
     };
+#pragma unroll 1
+    for (int r0 = part; r0 < rows; r0 += kBatch * parts) {
+      load(r0);
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (part + i * parts < rows) store(part + i * parts, x[i]);
-#pragma unroll 4
-    for (int r = part + kHeld * parts; r < rows; r += parts) {
-      Row4<T> y;
-      y.load(src, src_row + (size_t)r * p.H_kv, lane);
-      store(r, y);
+      for (int i = 0; i < kBatch; ++i)
+        if (r0 + i * parts < rows) store(r0 + i * parts, x[i]);
     }
   }
 }
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) copy_pages_q8_kernel(const CopyPages
 cudaError_t launch_append_q8(const AppendQ8Params& p, cudaStream_t stream) {
   const long long items = ((long long)p.num_new >> p.block_shift) + 2LL * p.num_seqs;
   if (items > 0x7fffffffLL) return cudaErrorNotSupported;
-  const int parts = (1 << p.block_shift) / kHeld < kWarps ? (1 << p.block_shift) / kHeld : kWarps;
+  const int parts = (1 << p.block_shift) / kWarpRows < kWarps ? (1 << p.block_shift) / kWarpRows : kWarps;
   const int pairs = kWarps / parts;                                // (head, K or V) pairs a CTA
   const long long groups = (2LL * p.H_kv + pairs - 1) / pairs;
   if (groups > 65535) return cudaErrorNotSupported;
