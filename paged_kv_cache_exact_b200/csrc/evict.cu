@@ -35,7 +35,7 @@ namespace pkv {
 namespace {
 
 // rows a thread has in flight: what fits 64 registers (four CTAs an SM)
-template <int kCache> constexpr int move_unroll() { return kCache == PKV_BF16 ? 8 : 4; }
+template <int kCache> constexpr int move_unroll() { return kCache == PKV_BF16 ? 6 : 4; }
 
 // float32 -> uint32 with the same order (-0 and +0 equal, NaN lowest).
 PKV_DEVINLINE uint32_t order_key(float f) {
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_
   __shared__ __align__(16) int hist[256];
   __shared__ uint32_t s_lo[kSelectWarps], s_hi[kSelectWarps], s_count[kSelectWarps];
   __shared__ int s_digit, s_need, s_here;
+  asm volatile("griddepcontrol.launch_dependents;");              // the move kernel may be scheduled
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int L = clamped_len(p, s);
   if (h == 0 && tid == 0) {
@@ -292,6 +293,7 @@ PKV_DEVINLINE void move_weights(const EvictParams& p) {
 
 template <int kCache, int kMoveThreads>
 __global__ void __launch_bounds__(kMoveThreads, 1024 / kMoveThreads) move_kernel(const EvictParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");              // the kept tokens and the scales are there
   constexpr int kMoveUnroll = move_unroll<kCache>();
   const int slices = p.row_bytes / p.slice_bytes;
   if ((int)blockIdx.x == 2 * slices) {
@@ -370,11 +372,22 @@ __global__ void __launch_bounds__(kMoveThreads, 1024 / kMoveThreads) move_kernel
 // us against 105; 576 CTAs, 8 long sequences: 94 against 68).
 template <int kCache>
 cudaError_t launch_move(const EvictParams& p, dim3 grid, cudaStream_t stream) {
-  if ((long long)grid.x * grid.y * grid.z <= 148LL * 4)
-    move_kernel<kCache, 256><<<grid, 256, 0, stream>>>(p);
-  else
-    move_kernel<kCache, 128><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  // Few CTAs are launched as a programmatic dependent of the selection, scheduled
+  // while that drains (one short sequence 12.4 -> 10.3 us).  More than an SM each
+  // would pile up on the SMs that are free first (32 sequences 119 -> 127 us).
+  const long long ctas = (long long)grid.x * grid.y * grid.z;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas <= 148 ? 1 : 0;
+  const bool wide = ctas <= 148LL * 4;
+  cfg.blockDim = dim3(wide ? 256 : 128);
+  return wide ? cudaLaunchKernelEx(&cfg, move_kernel<kCache, 256>, p)
+              : cudaLaunchKernelEx(&cfg, move_kernel<kCache, 128>, p);
 }
 
 template <int kKeys, int kSelectThreads>

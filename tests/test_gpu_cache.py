@@ -708,6 +708,48 @@ def test_evict_flags_bad_pages_and_lengths():
     assert torch.equal(got[4, :8], k[4, :8]) and torch.equal(got[4, 8:16], k[7, 8:16])
 
 
+@pytest.mark.parametrize("dtype", [BF16, I8], ids=["bf16", "i8"])
+def test_evict_captured_and_replayed_on_two_streams(dtype):
+    """Two captured evictions over one pool (other pages, weights and workspaces), replayed at once, thrice."""
+    gen = torch.Generator().manual_seed(9)
+    table, pages = tables([900, 1300, 700, 2000], 32, 1)
+    k, ks = pool(dtype, pages, 32, 16, 3, gen)
+    v, vs = pool(dtype, pages, 32, 16, 3, gen)
+    w = torch.rand((4, 3, 2000), generator=gen)
+    first = [x if x is None else x.to(DEV) for x in (k, v, ks, vs, w)]
+    live = [x if x is None else x.clone() for x in first]
+    lens = torch.tensor([900, 1300, 700, 2000], dtype=torch.int32, device=DEV)
+    table = table.to(DEV)
+
+    def run(x, rows, ws=None):
+        at = slice(*rows)
+        return api.evict(x[0], x[1], x[4][at], table[at], lens[at], 300, 50, 2000, k_scales=x[2], v_scales=x[3],
+                         workspace=ws)
+
+    want = [x if x is None else x.clone() for x in first]
+    kept = [run(want, r)[0] for r in ((0, 2), (2, 4))]
+    n = B.paged_kv_evict_workspace_size(2, 3, 300, 16, B.PKV_I8)
+    graphs, got, spaces = [], [], [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    for i, r in enumerate(((0, 2), (2, 4))):
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got.append(run(live, r, spaces[i] if dtype == I8 else None)[0])
+        graphs.append((g, s))
+    for rep in range(3):
+        for x, y in zip(live, first):
+            if x is not None:
+                x.copy_(y)
+        torch.cuda.synchronize()
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, kept))
+        assert all(torch.equal(raw(a), raw(b)) for a, b in zip(live, want) if a is not None)
+
+
 # ------------------------------------------------------------------ used together --
 
 
