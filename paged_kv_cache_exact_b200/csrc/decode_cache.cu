@@ -32,7 +32,8 @@
 // below 2^-24 of the largest, whose error is under 2^-39 of it).  P is rounded to
 // f16, lifted by 2^7 against the reference maximum so that weights down to 2^-21
 // of the largest keep all 11 bits and those below 2^-32 of it vanish.  A bf16 cache runs on bf16
-// products and P in bf16, as in the other decode kernels.  Scales are applied
+// products with P in two bf16 parts (16 bits: one part alone would be off by up to
+// 2^-8 where a few keys share the weight, and the pipe has room).  Scales are applied
 // in float32: ks to the score, vs to each chunk's P V product (a chunk of 16
 // tokens lies in one block).  Sums and maxima are float32; the reference
 // maximum moves only when a score passes it by 2^8 (O and l share it: exact).
@@ -441,7 +442,7 @@ cache_decode_kernel(const CacheAttnParams p) {
         }
     }
     // P^T as the B operand: column n = head, rows = the chunk's tokens
-    uint32_t pb[U][NT][2];
+    uint32_t pb[U][NT][2], plo[kBf16 ? NT : 1][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -454,8 +455,18 @@ cache_decode_kernel(const CacheAttnParams p) {
           pr[2 + j] = ex2(sc[u][nt][2 + j] - ref);
           l[nt][j] += pr[j] + pr[2 + j];
         }
-        pb[u][nt][0] = transpose8x8(kBf16 ? pack_bf16x2(pr[0], pr[1]) : pack_f16x2(pr[0], pr[1]));
-        pb[u][nt][1] = transpose8x8(kBf16 ? pack_bf16x2(pr[2], pr[3]) : pack_f16x2(pr[2], pr[3]));
+        if (kBf16) {                                         // what bf16 leaves of P goes in a second product
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t hi = pack_bf16x2(pr[2 * e], pr[2 * e + 1]);
+            pb[u][nt][e] = transpose8x8(hi);
+            plo[kBf16 ? nt : 0][e] =
+                transpose8x8(pack_bf16x2(pr[2 * e] - bf16lo(hi), pr[2 * e + 1] - bf16hi(hi)));
+          }
+        } else {
+          pb[u][nt][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+          pb[u][nt][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
+        }
       }
     }
     // O^T += vs V^T P^T
@@ -468,8 +479,10 @@ cache_decode_kernel(const CacheAttnParams p) {
         const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
         const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           mma16816<false>(o[nt][i], a0, a1, a2, a3, pb[0][nt][0], pb[0][nt][1]);
+          mma16816<false>(o[nt][i], a0, a1, a2, a3, plo[nt][0], plo[nt][1]);
+        }
       }
     } else {
 #pragma unroll

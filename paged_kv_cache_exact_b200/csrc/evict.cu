@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kMoveThreads, 1024 / kMoveThreads) move_kernel
 
 // At most 64 registers: an SM holds four CTAs of 256 threads or eight of 128.  The
 // wide ones have more rows in flight where all CTAs run at once; beyond that the
-// narrow ones waste less of the last turn (1280 CTAs, 32 sequences x 8 heads: 100
-// us against 105; 576 CTAs, 8 long sequences: 94 against 68).
+// narrow ones waste less of the last turn (1280 CTAs, 32 sequences x 8 heads: 105 us
+// wide, 100 narrow; 576 CTAs, 8 long sequences: 68 us wide, 94 narrow).
 template <int kCache>
 cudaError_t launch_move(const EvictParams& p, dim3 grid, cudaStream_t stream) {
   // Few CTAs are launched as a programmatic dependent of the selection, scheduled

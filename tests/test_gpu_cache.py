@@ -3,7 +3,8 @@
 Tolerances.  Rounding to a type is off by at most half a step, relative 2^-8 for
 bf16 and 2^-11 for f16.  An output element is sum_j p_j v_j: its own rounding
 gives 2^-8 |o|; rounding each p to the type of the product gives at most 2^-8
-(bf16 cache) or 2^-11 (8-bit cache) of sum_j p_j |v_j|.  A score is a float32
+(bf16, in the prefill kernel), 2^-11 (f16, few rows over an 8-bit cache) or 2^-15
+(two bf16 parts, few rows over a bf16 cache; taken as 2^-11) of sum_j p_j |v_j|.  A score is a float32
 sum of 128 products, off by at most 128 * 2^-24 of sum |q||k| * scale (and a few
 2^-24 of itself for its scales); an error e of every score changes p by a factor
 within exp(2 e), and 2^-20 covers the exponential, the sums and the division.  A
@@ -108,8 +109,8 @@ class Cache:
         want, ww, spread, size = attend(self.q, self.k, self.v, self.ks, self.vs, self.table, lens, causal, self.scale)
         e = 128 * 2.0 ** -24 * size
         rel = math.expm1(2 * e) + 2.0 ** -20
-        # P is rounded to bf16 for a bf16 cache and in the prefill kernel (many rows), else to f16
-        p_round = 2.0 ** -8 if self.dtype == BF16 or self.q.shape[2] > 1 else 2.0 ** -11
+        # which kernel takes several rows is the library's choice: the looser of the two bounds
+        p_round = 2.0 ** -8 if self.q.shape[2] > 1 else 2.0 ** -11
         tol = 2.0 ** -8 * want.abs() + (p_round + rel) * 1.01 * spread + 1e-30
         err = (out.double() - want).abs()
         assert torch.isfinite(out).all()
