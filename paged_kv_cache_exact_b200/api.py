@@ -9,9 +9,14 @@ codes in int8 or float8_e4m3fn pages and one float32 scale for each block of
 tokens and kv head; ``paged_weights`` and ``evict`` keep a cache within a budget
 of tokens.  These five check their tensors, raise ValueError or TypeError for
 ones that do not fit together, and run on the tensors' device whichever device
-is current.  With ``stream`` None they run on that device's current stream;
-another stream the caller orders against the tensors' producers and consumers
-(what these functions allocate themselves is kept for that stream's work).
+is current.
+
+With ``stream`` None a call runs on the current stream (these five: of the
+tensors' device).  Another stream the caller orders against the producers of the
+tensors that are passed and the consumers of the results.  What a call allocates
+it takes from its own stream's memory, which no other stream's earlier work can
+still be using; results may be dropped on the stream that is current at the call,
+and elsewhere by torch's rules (``record_stream``).
 """
 
 from __future__ import annotations
@@ -26,6 +31,32 @@ from . import binding as B
 _DT = {torch.bfloat16: B.PKV_BF16, torch.float32: B.PKV_F32}
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _torch_stream(stream, device):
+    return stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(B._stream(stream), device=device)
+
+
+def _allocating(stream, device):
+    """A context whose torch allocations come from `stream`'s memory (None: the current stream's)."""
+    return _HERE if stream is None else torch.cuda.stream(_torch_stream(stream, device))
+
+
+def _used_on(stream, passed=(), made=()):
+    """Keep tensors from being reused before work that their own stream does not know of has run: the call's for
+    those that were passed, the caller's for those that the call made."""
+    if stream is None:
+        return
+    for t in passed:
+        if t is not None:
+            t.record_stream(_torch_stream(stream, t.device))
+    for t in made:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype not in _DT:
         raise TypeError(f"unsupported dtype {t.dtype}")
@@ -37,7 +68,11 @@ def prefill(Q, K, V, causal: bool, scale: float, out=None, stream=None) -> torch
     Bn, H, N, d = Q.shape
     for t in (Q, K, V):
         assert t.is_contiguous() and t.shape == Q.shape and t.dtype == Q.dtype
-    O = torch.empty_like(Q) if out is None else out
+    O = out
+    if O is None:
+        with _allocating(stream, Q.device):
+            O = torch.empty_like(Q)
+        _used_on(stream, made=(O,))
     B.attn_prefill(Q, K, V, O, Bn, H, N, d, causal, scale, _dtype(Q), stream)
     return O
 
@@ -58,10 +93,14 @@ def paged(q, k_pages, v_pages, block_table, seq_lens, page_size: int, causal: bo
     assert ps == page_size and d2 == d and v_pages.shape == k_pages.shape
     assert block_table.dtype == torch.int32 and seq_lens.dtype == torch.int32
     assert block_table.is_contiguous() and q.is_contiguous() and k_pages.is_contiguous()
-    o = torch.empty_like(q) if out is None else out
-    ws = workspace
+    o, ws = out, workspace
+    if o is None:
+        with _allocating(stream, q.device):
+            o = torch.empty_like(q)
+        _used_on(stream, made=(o,))
     if ws is None and q_len == 1:
-        ws = workspace_for(S, H, d, max_seq_len, page_size, q.device)
+        with _allocating(stream, q.device):
+            ws = workspace_for(S, H, d, max_seq_len, page_size, q.device)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     B.paged_attn(q, k_pages, v_pages, block_table, seq_lens, page_size, S, q_len, H, H_kv, d,
                  P, block_table.shape[1], max_seq_len, causal, scale, _dtype(q), o, ws,
@@ -77,9 +116,6 @@ _Q8 = {torch.int8: B.PKV_I8, torch.float8_e4m3fn: B.PKV_E4M3}
 def _need(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
-
-
-_HERE = contextlib.nullcontext()
 
 
 def _on_device(*tensors):
@@ -122,20 +158,12 @@ def _int32(*tensors):
 
 
 def _workspace(workspace, n, device):
+    """(workspace, its bytes); one that is made here is used by the call's stream alone."""
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor of the same device")
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
-def _used_on(stream, *tensors):
-    """Keep what was allocated here from being reused before another stream's work has run."""
-    if stream is not None:
-        st = torch.cuda.ExternalStream(B._stream(stream), device=tensors[0].device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(st)
 
 
 # Sizes alone decide a workspace's bytes.
@@ -184,9 +212,8 @@ def _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out):
     _int32(block_table, seq_lens)
     _need(block_table.dim() == 2 and block_table.shape[0] == S and seq_lens.numel() == S,
           "block_table and seq_lens must hold a row and a length for each sequence")
-    o = torch.empty_like(q) if out is None else out
-    _need(o.shape == q.shape and o.dtype == q.dtype, "out must look like q")
-    return S, H, q_len, d, H_kv, o
+    _need(out is None or (out.shape == q.shape and out.dtype == q.dtype), "out must look like q")
+    return S, H, q_len, d, H_kv
 
 
 def paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size: int, causal: bool,
@@ -195,14 +222,16 @@ def paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, pag
     cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
     if cache not in (B.PKV_I8, B.PKV_E4M3):
         raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
-    S, H, q_len, d, H_kv, o = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
-    with _on_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, o):
-        ws, n = _workspace(workspace, _q8_bytes(S, q_len, H, H_kv, max_seq_len, page_size),
-                           q.device)
+    S, H, q_len, d, H_kv = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
+    mine = () if out is None else (out,)
+    with _on_device(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, *mine):
+        with _allocating(stream, q.device):
+            o = torch.empty_like(q) if out is None else out
+            ws, n = _workspace(workspace, _q8_bytes(S, q_len, H, H_kv, max_seq_len, page_size), q.device)
         B.paged_attn_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S, q_len,
                         H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale, cache, o,
                         ws, n, _stream_of(stream, q))
-        _used_on(stream, o, ws)
+        _used_on(stream, (out, workspace), () if out is not None else (o,))
     return o
 
 
@@ -212,17 +241,18 @@ def paged_weights(q, k_pages, v_pages, block_table, seq_lens, page_size: int, ca
     """Attention over a bf16 or 8-bit paged cache that adds every key's softmax weight, summed over the
     query rows and the query heads of its kv head, to ``weights`` [S, H_kv, >= max_seq_len] (float32)."""
     cache, block = _pools(k_pages, v_pages, k_scales, v_scales)
-    S, H, q_len, d, H_kv, o = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
+    S, H, q_len, d, H_kv = _attn_shapes(q, k_pages, block_table, seq_lens, page_size, out)
     _need(weights.dtype == torch.float32 and weights.dim() == 3 and weights.shape[:2] == (S, H_kv)
           and weights.shape[2] >= max_seq_len, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
-    more = () if block == 0 else (k_scales, v_scales)
-    with _on_device(q, k_pages, v_pages, block_table, seq_lens, o, weights, *more):
-        ws, n = _workspace(workspace, _weights_bytes(S, q_len, H, H_kv, max_seq_len, page_size),
-                           q.device)
+    more = (() if block == 0 else (k_scales, v_scales)) + (() if out is None else (out,))
+    with _on_device(q, k_pages, v_pages, block_table, seq_lens, weights, *more):
+        with _allocating(stream, q.device):
+            o = torch.empty_like(q) if out is None else out
+            ws, n = _workspace(workspace, _weights_bytes(S, q_len, H, H_kv, max_seq_len, page_size), q.device)
         B.paged_attn_weights(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, page_size, block, S,
                              q_len, H, H_kv, d, k_pages.shape[0], block_table.shape[1], max_seq_len, causal, scale,
                              cache, o, weights, weights.shape[2], ws, n, _stream_of(stream, q))
-        _used_on(stream, o, ws)
+        _used_on(stream, (out, workspace), () if out is not None else (o,))
     return o
 
 
@@ -246,11 +276,12 @@ def evict(k_pages, v_pages, weights, block_table, seq_lens, budget: int, recent:
           and weights_out.dtype == torch.float32, "weights must be float32 [num_seqs, H_kv, >= max_seq_len]")
     more = () if block == 0 else (k_scales, v_scales)
     with _on_device(k_pages, v_pages, weights, weights_out, block_table, dst_table, seq_lens, *more):
-        kept = seq_lens.new_empty((S, H_kv, max(budget, 0)))
-        new_lens = torch.empty_like(seq_lens)
-        ws, n = _workspace(workspace, _evict_bytes(S, H_kv, budget, block, cache), k_pages.device)
+        with _allocating(stream, k_pages.device):
+            kept = torch.empty((S, H_kv, max(budget, 0)), dtype=torch.int32, device=k_pages.device)
+            new_lens = torch.empty_like(seq_lens)
+            ws, n = _workspace(workspace, _evict_bytes(S, H_kv, budget, block, cache), k_pages.device)
         B.paged_kv_evict(k_pages, v_pages, k_scales, v_scales, weights, weights_out, weights.shape[2], block_table,
                          dst_table, seq_lens, new_lens, kept, budget, recent, S, H_kv, d, P, ps, block,
                          block_table.shape[1], max_seq_len, cache, ws, n, _stream_of(stream, k_pages))
-        _used_on(stream, kept, new_lens, ws)
+        _used_on(stream, (workspace,), (kept, new_lens))
     return kept, new_lens

@@ -1,0 +1,76 @@
+"""Corners of the 8-bit paged cache, attention weights and eviction on the GPU: other streams, values that
+are not finite, scales of zero, wide tables, many evictions.  Tolerances are those of test_gpu_cache.py
+where a check does not say its own."""
+
+import pytest
+import torch
+
+from paged_kv_cache_exact_b200 import api
+from paged_kv_cache_exact_b200 import binding as B
+from test_gpu_cache import BF16, DEV, I8, Cache, _errors, raw  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def busy():
+    """Some milliseconds of work on the current stream."""
+    x = torch.zeros((4096, 4096), dtype=BF16, device=DEV)
+    for _ in range(100):
+        x = x @ x
+
+
+@pytest.mark.parametrize("op", ["attend", "weights", "evict"])
+def test_another_streams_results_do_not_share_freed_memory(op):
+    """A call on another stream, which waits for its inputs alone, while work that the current stream still has to do
+    writes blocks of the results' sizes that were freed a moment ago."""
+    c = Cache(I8, [700, 40, 1300], 16, 2, 16, 16, seed=9)
+    first = [x.clone() for x in (c.k, c.v, c.ks, c.vs, c.w)]
+
+    def run(**kw):
+        if op == "attend":
+            return (c.run(False, **kw),)
+        if op == "weights":
+            return c.run(True, **kw), c.w
+        return api.evict(c.k, c.v, c.w, c.table, c.len_t, 90, 8, 1300, k_scales=c.ks, v_scales=c.vs, **kw) + (c.w, c.k)
+
+    want = [x.clone() for x in run()]
+    for x, y in zip((c.k, c.v, c.ks, c.vs, c.w), first):
+        x.copy_(y)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    made = [x for x in want if x.shape not in (c.w.shape, c.k.shape)]
+    n = B.paged_attn_weights_workspace_size(3, 1, 16, 2, 1300, 16)
+    busy()
+    freed = [torch.empty_like(x) for x in made] + [torch.empty(n, dtype=torch.uint8, device=DEV)]
+    for x in freed:
+        x.fill_(77)
+    at = {x.data_ptr() for x in freed}
+    del freed, x
+    got = run(stream=s)
+    torch.cuda.synchronize()
+    assert not at & {x.data_ptr() for x in got[:len(made)]}
+    assert all(torch.equal(raw(a), raw(b)) for a, b in zip(got, want))
+
+
+def test_results_of_another_stream_outlive_their_name():
+    """A result that is dropped while the current stream still has to read it is not handed to the other stream."""
+    c = Cache(I8, [900, 31], 16, 2, 16, 16, seed=10)
+    want = c.run(False)
+    s = torch.cuda.Stream()
+    busy()
+    (want + 0).fill_(5)                    # what is used below is loaded: loading waits for the device
+    with torch.cuda.stream(s):
+        torch.empty_like(want)
+    torch.cuda.synchronize()
+    out = c.run(False, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    busy()
+    copy = out + 0
+    at = out.data_ptr()
+    del out
+    with torch.cuda.stream(s):
+        other = torch.empty_like(want).fill_(5)
+    assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
