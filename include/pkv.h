@@ -335,7 +335,8 @@ PKV_API int paged_kv_copy_pages(void* k_pages, void* v_pages, const int32_t* src
  * no value is ever clipped, and codes change only where a scale grows.  A block
  * that takes in a NaN or an infinity gets scale NaN and codes 0, and stays NaN
  * until its first token is written anew: rows that see the block get NaN from
- * attention over it (and so do the weights that they give), others do not.
+ * attention over it, others do not.  The weights that a row gives (below) become
+ * NaN with a block of K, and do not depend on V.
  *
  * k_new, v_new, cu_new, start_pos, block_table, num_new, num_seqs and the pool's
  * sizes mean what they mean in paged_kv_append.  dtype is the new rows' type,

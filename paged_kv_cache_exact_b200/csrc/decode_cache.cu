@@ -364,9 +364,19 @@ cache_decode_kernel(const CacheAttnParams p) {
       tok[u] = t_begin + 16 * cu;
       page_ok[u] = cu < n_chunks && s_pages[(tok[u] >> p.page_shift) - lp0] >= 0;
       scales[u] = kBf16 ? make_float2(1.f, 1.f) : *reinterpret_cast<const float2*>(s_scale[warp][now][u]);
-      // A NaN value scale makes every row that sees the block NaN; said through the
-      // key scale, which masking keeps from rows that do not see it.
-      if (!kBf16 && isnan(scales[u].y)) scales[u] = make_float2(scales[u].y, 1.f);
+      // A NaN value scale makes the output of every row that sees the block NaN.  Said
+      // to O here, it reaches neither the other rows (P = 0 times NaN) nor the weights.
+      if (!kBf16 && isnan(scales[u].y)) {                    // the same on every lane
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            if (tok[u] < end[nt][j]) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[nt][i][j] = o[nt][i][2 + j] = scales[u].y;
+            }
+        scales[u].y = 1.f;
+      }
     }
     // S^T = K Q^T, in two chains of four steps
     float sc[U][NT][4], sd[U][NT][4];

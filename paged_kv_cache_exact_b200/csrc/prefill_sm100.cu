@@ -834,12 +834,8 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUten
             vs[4 * i] = b.x, vs[4 * i + 1] = b.y, vs[4 * i + 2] = b.z, vs[4 * i + 3] = b.w;
           }
 #pragma unroll
-          for (int b = 0; b < 8; ++b) {
+          for (int b = 0; b < 8; ++b)
             if (ks[b] < 0.f) bad_keys[b >> 1] |= 0xFFFFu << (16 * (b & 1));
-            // A NaN value scale makes every row that sees the block NaN; said through
-            // the key scale, which masking keeps from rows that do not see it.
-            if (isnan(vs[b])) ks[b] = vs[b], vs[b] = 1.f;
-          }
         } else if (kPaged) {
           // Keys of pages outside the pool are left out (their K rows were
           // never loaded).  The loader wrote this tile's mask before its K load.
@@ -901,7 +897,12 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& tmQ, const CUten
           }
           if (kQ8) {
 #pragma unroll
-            for (int b = 0; b < 8; ++b) ks[b] = 1.f;      // applied above
+            for (int b = 0; b < 8; ++b) {
+              ks[b] = 1.f;                                // applied above
+              // A NaN value scale makes the output of every row that sees the block NaN,
+              // through P; a row that does not see it must not multiply its P = 0 by it.
+              if (k0 + 16 * b > limit) vs[b] = 1.f;
+            }
           }
         }
         // row max: eight chains of 3-input max (dependency depth 8)

@@ -2,12 +2,15 @@
 are not finite, scales of zero, wide tables, many evictions.  Tolerances are those of test_gpu_cache.py
 where a check does not say its own."""
 
+import math
+
 import pytest
 import torch
 
+from _cache_ref import attend
 from paged_kv_cache_exact_b200 import api
 from paged_kv_cache_exact_b200 import binding as B
-from test_gpu_cache import BF16, DEV, I8, Cache, _errors, raw  # noqa: F401
+from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, raw  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +77,42 @@ def test_results_of_another_stream_outlive_their_name():
     assert other.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+# ------------------------------------------------------------------- values that are not finite --
+
+
+def check_weights(c, before, size, want):
+    """The weights that a call added, against float64 ones, by the bound of test_gpu_cache.py."""
+    rel = math.expm1(2 * 128 * 2.0 ** -24 * size) + 2.0 ** -20
+    for s, n in enumerate(c.lens):
+        got = c.w[s, :, :n].double() - before[s, :, :n].double()
+        rel_w = rel + 2.0 ** -23 * (1.4427 * size + math.log2(max(n, 2)))
+        tol = rel_w * 1.01 * want[s] + 2.0 ** -24 * (c.w[s, :, :n].double().abs() + before[s, :, :n].double())
+        assert ((got - want[s]).abs() <= tol).all(), f"weights of {s}"
+        assert torch.equal(c.w[s, :, n:], before[s, :, n:])
+
+
+@pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
+@pytest.mark.parametrize("q_len,lens,key", [
+    (1, [100, 70], 96),                 # one split
+    (1, [5000, 70], 2048),              # several splits
+    (1, [40, 33], 0),
+    (12, [100, 70], 96),                # seen from row 8 on
+    (100, [100, 300], 48),              # the prefill kernel
+    (300, [700, 300], 448),             # the block of a later tile: 52 rows do not see it
+])
+def test_a_nan_value_scale_leaves_the_weights_alone(dtype, q_len, lens, key):
+    """The rows that see the block become NaN and no others; softmax weights, which the values do not enter, stay what
+    the keys make them."""
+    c = Cache(dtype, lens, 4, 2, 16, 16, q_len=q_len, seed=24)
+    _, want, _, size = attend(c.q, c.k, c.v, c.ks, c.vs, c.table, lens, True, c.scale)
+    c.vs[int(c.table[0, key // 16]), 0, 1] = float("nan")
+    before = c.w.clone()
+    out = c.run(True)
+    first = max(0, key - (lens[0] - q_len))                          # the first row that sees the block
+    assert torch.isnan(out[0, 2:, first:]).all()
+    assert torch.isfinite(out[0, :2]).all() and torch.isfinite(out[0, 2:, :first]).all() and torch.isfinite(out[1]).all()
+    check_weights(c, before, size, want)
+    again = c.run(False)
+    assert torch.equal(torch.isnan(again), torch.isnan(out))
