@@ -704,12 +704,14 @@ PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, i
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
   const float2* ml = p.ws_ml + ((size_t)s * p.H + kvh * group) * p.max_splits;
   // no visible key: every score is -inf, and 2^(-inf - 0) = 0
+  bool broken = false;                            // this thread's row saw a NaN
   if (group <= kWeightThreads / 32) {             // a warp a row
     const int h = threadIdx.x >> 5;
     if (h < group) {
       float M, lsum;
       merge_ml(ml + (size_t)h * p.max_splits, nsplit, threadIdx.x & 31, M, lsum);
       if ((threadIdx.x & 31) == 0) s_lse[h] = lsum == 0.f ? 0.f : M + log2f(lsum);
+      broken = isnan(lsum);
     }
   } else if (threadIdx.x < group) {               // a thread a row
     const float2* row = ml + (size_t)threadIdx.x * p.max_splits;
@@ -722,15 +724,29 @@ PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, i
       lsum = fmaf(v.x == -INFINITY && M == -INFINITY ? 1.f : ex2(v.x - M), v.y, lsum);
     }
     s_lse[threadIdx.x] = lsum == 0.f ? 0.f : M + log2f(lsum);
+    broken = isnan(lsum);
   }
-  __syncthreads();
+  const bool some_broken = __syncthreads_or(broken);
   const size_t sk = (size_t)s * p.H_kv + kvh;
   const float* lg = p.logits + sk * p.logit_tokens * group;
   float* w = p.weights + sk * p.weights_stride;
-  if (group == 8) return thread_weights<2>(lg, s_lse, w, t0, min(L, t0 + p.range_tokens));
-  if (group == 4) return thread_weights<1>(lg, s_lse, w, t0, min(L, t0 + p.range_tokens));
-  const int lanes = p.token_lanes, mine = threadIdx.x % lanes;
   const int t_end = min(L, t0 + p.range_tokens);
+  if (some_broken) {
+    // A NaN row gives NaN to the keys that it sees, and nothing to the others, whose
+    // score of -inf minus NaN would be NaN too: what a key is seen by is looked up.
+    for (int t = t0 + threadIdx.x; t < t_end; t += kWeightThreads) {
+      const int phys = p.block_table[(size_t)s * p.max_pages + (t >> p.page_shift)];
+      if (phys < 0 || phys >= p.num_pages) continue;
+      float sum = 0.f;
+      for (int h = 0; h < group; ++h)
+        if (!p.causal || t <= L - p.q_len + h % p.q_len) sum += ex2(lg[(size_t)t * group + h] - s_lse[h]);
+      w[t] += sum;
+    }
+    return;
+  }
+  if (group == 8) return thread_weights<2>(lg, s_lse, w, t0, t_end);
+  if (group == 4) return thread_weights<1>(lg, s_lse, w, t0, t_end);
+  const int lanes = p.token_lanes, mine = threadIdx.x % lanes;
   for (int t1 = t0; t1 < t_end; t1 += kWeightThreads / lanes) {              // a warp's trip count is uniform
     const int t = t1 + threadIdx.x / lanes;
     float sum = 0.f;

@@ -10,7 +10,7 @@ import torch
 from _cache_ref import attend
 from paged_kv_cache_exact_b200 import api
 from paged_kv_cache_exact_b200 import binding as B
-from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, raw  # noqa: F401
+from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, clean, raw  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,27 @@ def test_a_nan_value_scale_leaves_the_weights_alone(dtype, q_len, lens, key):
     check_weights(c, before, size, want)
     again = c.run(False)
     assert torch.equal(torch.isnan(again), torch.isnan(out))
+
+
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("H,H_kv", [(2, 2), (10, 2), (8, 2), (16, 2)])       # 1, 5, 4 and 8 heads a kv head
+@pytest.mark.parametrize("q_len", [1, 12, 90])
+def test_a_bad_page_gets_no_weight_from_rows_that_are_nan(dtype, q_len, H, H_kv):
+    """Whichever kernel takes the rows: keys of a page outside the pool, and keys past a row's own, get nothing."""
+    c = Cache(dtype, [200, 130], H, H_kv, 16, 16, q_len=q_len, seed=25)
+    c.table[0, 3] = 1 << 20                                          # keys 48 .. 63
+    page = int(c.table[0, 5])
+    if dtype == BF16:
+        c.k[page, 2, 1] = float("nan")
+    else:
+        c.ks[page, 0, 1] = float("nan")
+    before = c.w.clone()
+    out = c.run(True)
+    assert clean() == B.PKV_DEVERR_BAD_PAGE
+    G = H // H_kv
+    assert torch.isnan(out[0, G:]).all() and torch.isfinite(out[0, :G]).all() and torch.isfinite(out[1]).all()
+    assert torch.equal(c.w[0, :, 48:64], before[0, :, 48:64])
+    live = torch.ones(200, dtype=torch.bool)
+    live[48:64] = False
+    assert torch.isnan(c.w[0, 1, :200][live.to(DEV)]).all() and torch.isfinite(c.w[0, 0, :200]).all()
+    assert torch.equal(c.w[0, :, 200:], before[0, :, 200:])
