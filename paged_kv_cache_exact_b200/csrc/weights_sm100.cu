@@ -273,14 +273,15 @@ prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const CacheAttnPa
       if (!ok) break;
       tc_fence_after();
       const uint32_t tS = tmem + lane_addr + 128 * buf;
-      // first column (query row) of this tile that sees my key
+      // columns (query rows) of this tile that see my key
       const int q0 = (first_q + n % per_head) * BQ;
       const int first_col = p.causal ? k0 + r - off - q0 : 0;
+      const int end_col = p.q_len - q0;
       const float4* lse = reinterpret_cast<const float4*>(smem + kOffLse + st * kLseBytes);
       uint64_t acc[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] = f2(0.f, 0.f);
-      auto tile = [&](auto diagonal) {
+      auto tile = [&](auto edge) {
         uint32_t xs[2][32];
         tmem_ld32(tS, xs[0]);
         tmem_wait_ld();
@@ -288,28 +289,30 @@ prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const CacheAttnPa
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t (&x)[32] = xs[ch & 1];
           if (ch < 3) tmem_ld32(tS + 32 * (ch + 1), xs[(ch + 1) & 1]);         // lands while this quarter is summed
+          if (!decltype(edge)::value || 32 * ch < end_col) {       // else: no row in this quarter
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 e = lse[8 * ch + i];                      // minus lse; rows past q_len: -infinity, weight 0
-            const uint64_t y0 =
-                fma2(f2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), c2, f2(e.x, e.y));
-            const uint64_t y1 =
-                fma2(f2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), c2, f2(e.z, e.w));
-            if ((i == 1 || i == 5) && !decltype(diagonal)::value) {
-              acc[2 * (i & 1)] = exp2_pair_add(y0, acc[2 * (i & 1)]);
-              acc[2 * (i & 1) + 1] = exp2_pair_add(y1, acc[2 * (i & 1) + 1]);
-              continue;
-            }
-            float v[4];
-            unf2(y0, v[0], v[1]);
-            unf2(y1, v[2], v[3]);
-            if (decltype(diagonal)::value) {
+            for (int i = 0; i < 8; ++i) {
+              const float4 e = lse[8 * ch + i];                      // minus lse
+              const uint64_t y0 =
+                  fma2(f2(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), c2, f2(e.x, e.y));
+              const uint64_t y1 =
+                  fma2(f2(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), c2, f2(e.z, e.w));
+              if ((i == 1 || i == 5) && !decltype(edge)::value) {
+                acc[2 * (i & 1)] = exp2_pair_add(y0, acc[2 * (i & 1)]);
+                acc[2 * (i & 1) + 1] = exp2_pair_add(y1, acc[2 * (i & 1) + 1]);
+                continue;
+              }
+              float v[4];
+              unf2(y0, v[0], v[1]);
+              unf2(y1, v[2], v[3]);
+              if (decltype(edge)::value) {
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (32 * ch + 4 * i + b < first_col) v[b] = -INFINITY;
+                for (int b = 0; b < 4; ++b)
+                  if (32 * ch + 4 * i + b < first_col || 32 * ch + 4 * i + b >= end_col) v[b] = -INFINITY;
+              }
+              acc[2 * (i & 1)] = add2(acc[2 * (i & 1)], f2(ex2(v[0]), ex2(v[1])));
+              acc[2 * (i & 1) + 1] = add2(acc[2 * (i & 1) + 1], f2(ex2(v[2]), ex2(v[3])));
             }
-            acc[2 * (i & 1)] = add2(acc[2 * (i & 1)], f2(ex2(v[0]), ex2(v[1])));
-            acc[2 * (i & 1) + 1] = add2(acc[2 * (i & 1) + 1], f2(ex2(v[2]), ex2(v[3])));
           }
           if (ch < 3) tmem_wait_ld();
           if (ch == 2) {                                           // all of the tile is in registers
@@ -318,7 +321,9 @@ prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const CacheAttnPa
           }
         }
       };
-      if (p.causal && k0 + BK - 1 - off > q0) tile(std::true_type{});          // warp-uniform
+      // The diagonal, and a last tile that is not full: its rows past q_len are zeros,
+      // which an infinite key would turn into NaN.  Warp-uniform.
+      if ((p.causal && k0 + BK - 1 - off > q0) || end_col < BQ) tile(std::true_type{});
       else tile(std::false_type{});
       mbar_arrive(bar(kBarQEmpty + st));                           // lse read
       float lo, hi;

@@ -140,3 +140,22 @@ def test_a_bad_page_gets_no_weight_from_rows_that_are_nan(dtype, q_len, H, H_kv)
     live[48:64] = False
     assert torch.isnan(c.w[0, 1, :200][live.to(DEV)]).all() and torch.isfinite(c.w[0, 0, :200]).all()
     assert torch.equal(c.w[0, :, 200:], before[0, :, 200:])
+
+
+@pytest.mark.parametrize("q_len", [129, 200, 300])
+def test_prompt_weights_of_an_infinite_key(q_len):
+    """A key that scores minus infinity in every row gets no weight: rows past q_len, which a tile pads with zeros,
+    must not make it NaN (0 times infinity)."""
+    c = Cache(BF16, [q_len + 70], 4, 2, 16, 16, q_len=q_len, seed=26)
+    c.q[..., 5] = c.q[..., 5].abs() + 0.25
+    n = q_len + 70
+    _, want, _, size = attend(c.q, c.k, c.v, None, None, c.table, [n], True, c.scale)
+    key = 40                                                         # seen by every row
+    c.k[int(c.table[0, key // 16]), key % 16, 0, 5] = -float("inf")
+    _, want, _, _ = attend(c.q, c.k, c.v, None, None, c.table, [n], True, c.scale)
+    assert torch.isfinite(want[0]).all() and (want[0][0, key] == 0).all()
+    before = c.w.clone()
+    out = c.run(True)
+    assert torch.isfinite(out).all()
+    check_weights(c, before, size, want)
+    assert torch.equal(c.w[0, 0, key], before[0, 0, key])
