@@ -448,7 +448,8 @@ PKV_API int paged_attn_weights(const void* q, const void* k_pages, const void* v
  *               block_tokens are not looked at), PKV_I8 or PKV_E4M3 (d 128).
  *               An 8-bit block's new scale is the largest of its rows' scales,
  *               and a row of another scale gets nearest(code * s_old / s_new);
- *               a NaN scale makes the block NaN with codes 0.
+ *               a NaN scale makes the block NaN with codes 0.  Scales are >= 0 or
+ *               NaN; a zero scale (rows of zeros) moves like any other.
  * workspace   : >= paged_kv_evict_workspace_size() bytes, 256-byte aligned (NULL
  *               if that size is 0), one for each call in flight.
  * A token whose page is outside the pool is not moved, and a length outside its

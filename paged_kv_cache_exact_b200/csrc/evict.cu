@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_
   __syncthreads();
   for (int j = tid; j < m; j += kSelectThreads) {
     const int t = kept[j];
-    float2 v = make_float2(0.f, 0.f);
+    float2 v = make_float2(-1.f, -1.f);             // a row that is not moved has no say
     const long long r = token_row(p, p.block_table, s, t);
     if (r >= 0) {
       const size_t i = (size_t)(r >> p.block_shift) * p.H_kv + h;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_
   const int bt = 1 << p.block_shift;
   const int blocks = (m + bt - 1) >> p.block_shift;
   for (int b = warp; b < blocks; b += kSelectWarps) {
-    float k = 0.f, v = 0.f;
+    float k = -1.f, v = -1.f;
     for (int j = (b << p.block_shift) + lane; j < min(m, (b + 1) << p.block_shift); j += 32) {
       const float2 r = row_scale[j];
       k = max_nan(k, r.x);
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_
     if (lane == 0) {
       p.block_scale[sh * p.max_blocks + b] = make_float2(k, v);
       const long long r = token_row(p, p.dst_table, s, b << p.block_shift);
-      if (r >= 0 && k != 0.f) {
+      if (r >= 0 && k != -1.f) {                    // some row is moved
         const size_t i = (size_t)(r >> p.block_shift) * p.H_kv + h;
         p.k_scales[i] = k;
         p.v_scales[i] = v;

@@ -7,10 +7,10 @@ import math
 import pytest
 import torch
 
-from _cache_ref import attend
+from _cache_ref import attend, evict, nearest
 from paged_kv_cache_exact_b200 import api
 from paged_kv_cache_exact_b200 import binding as B
-from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, clean, raw  # noqa: F401
+from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, clean, pool, raw  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,46 @@ def test_prompt_weights_of_an_infinite_key(q_len):
     assert torch.isfinite(out).all()
     check_weights(c, before, size, want)
     assert torch.equal(c.w[0, 0, key], before[0, 0, key])
+
+
+# ------------------------------------------------------------------------------- eviction --
+
+
+@pytest.mark.parametrize("place", ["in place", "to fresh pages"])
+@pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
+@pytest.mark.parametrize("zero", ["k", "v", "both"])
+def test_evict_moves_blocks_of_scale_zero(dtype, place, zero):
+    """Some blocks' scales are zero (their rows stand for zeros): K's scale says nothing about V's, and a destination
+    block's old scale does not stay behind."""
+    gen = torch.Generator().manual_seed(31)
+    L, budget, ps, H_kv = 160, 64, 16, 2
+    table = torch.randperm(10, generator=gen).to(torch.int32)[None]
+    dst = table.clone()
+    if place != "in place":
+        dst[0, :4] = torch.arange(10, 14)
+    k, ks = pool(dtype, 14, ps, 16, H_kv, gen)
+    v, vs = pool(dtype, 14, ps, 16, H_kv, gen)
+    for x, name in ((ks, "k"), (vs, "v")):
+        if zero in (name, "both"):
+            for b in (0, 2, 3, 4, 5, 6, 7):
+                x[int(table[0, b])] = 0
+    w = torch.rand((1, H_kv, L), generator=gen)
+    g = [x.to(DEV) for x in (k, v, w, table, torch.tensor([L], dtype=torch.int32), dst, ks, vs)]
+    kept, _ = api.evict(g[0], g[1], g[2], g[3], g[4], budget, 8, L, dst_table=g[5], k_scales=g[6], v_scales=g[7])
+    ids = evict(w, [L], budget, 8)
+    for h in range(H_kv):
+        i = torch.tensor(ids[0][h])
+        assert kept[0, h].tolist() == ids[0][h]
+        of = (table[0].long()[i // ps], i % ps, torch.full_like(i, h))
+        j = torch.arange(budget)
+        to = (dst[0].long()[j // ps], j % ps, torch.full_like(j, h))
+        for codes, scales, now, now_s in ((k, ks, g[0], g[6]), (v, vs, g[1], g[7])):
+            old = scales[of[0], 0, h]
+            new = old.view(-1, 16).amax(-1)
+            assert torch.equal(now_s.cpu()[dst[0, :4].long(), 0, h], new)
+            new = new.repeat_interleave(16).double()
+            y = codes[of].double() if dtype == I8 else raw(codes)[of].view(dtype).double()
+            exp = torch.where(new[:, None] > 0, nearest((y * old.double()[:, None]) / new.clamp(min=1e-300)[:, None],
+                                                        dtype), 0) * new[:, None]
+            got = raw(now).cpu()[to].view(dtype).double() * new[:, None]
+            assert torch.equal(got, exp)
