@@ -168,7 +168,7 @@ cache_decode_kernel(const CacheAttnParams p) {
   for (int i = 0; i < kMaxSplitPages / kThreads; ++i)
     mine_lp[i] = tid + i * kThreads < n_lp ? p.block_table[(size_t)s * p.max_pages + lp0 + tid + i * kThreads] : -1;
   int L = p.seq_lens[s];
-  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
   if (L < q_len || L > cap) {
     if (split == 0 && blockIdx.x == 0 && tid == 0) flag_error(p.err, PKV_DEVERR_BAD_LEN);
     L = max(0, min(L, cap));
@@ -612,7 +612,7 @@ PKV_DEVINLINE void merge_rows(const CacheAttnParams& p, int cta) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mw = p.merge_warps, part = warp % mw;
   const long long sh = (long long)cta * (kMergeWarps / mw) + warp / mw;
-  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
   const bool row = sh < (long long)p.num_seqs * p.H;
   const int L = row ? max(0, min(p.seq_lens[sh / p.H], cap)) : 0;
   const int nsplit = (L + p.split_tokens - 1) / p.split_tokens;
@@ -696,7 +696,7 @@ PKV_DEVINLINE void thread_weights(const float* lg, const float* s_lse, float* w,
 // group's rows of 2^(x - lse).
 PKV_DEVINLINE void range_weights(const CacheAttnParams& p, int range, int kvh, int s) {
   __shared__ __align__(16) float s_lse[kMaxGroup];
-  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
   const int L = max(0, min(p.seq_lens[s], cap));
   const int t0 = range * p.range_tokens;
   if (t0 >= L) return;

@@ -45,7 +45,7 @@ PKV_DEVINLINE uint32_t order_key(float f) {
 }
 
 PKV_DEVINLINE int clamped_len(const EvictParams& p, int s) {
-  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
   return max(0, min(p.seq_lens[s], cap));
 }
 

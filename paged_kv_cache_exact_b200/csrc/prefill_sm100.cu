@@ -194,7 +194,7 @@ __device__ __forceinline__ Geometry item_geometry(const PrefillParams& p, int it
   g.bad_len = false;
   if (p.paged) {
     kv_len = p.seq_lens[g.b];
-    const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+    const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
     if (kv_len < p.q_len || kv_len > cap) {
       g.bad_len = true;
       kv_len = max(0, min(kv_len, cap));

@@ -130,7 +130,7 @@ prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const CacheAttnPa
   const int s = blockIdx.z, kvh = blockIdx.x;
   const int k0 = blockIdx.y * BK;
   const int group = p.H / p.H_kv;
-  const int cap = min(p.max_seq_len, p.max_pages * p.page_size);
+  const int cap = p.max_seq_len;                   // the table holds at least as many tokens (checked by the host)
   const int kv_len = max(0, min(p.seq_lens[s], cap));              // the prefill kernel flags a bad length
   if (k0 >= kv_len) return;
   const int off = kv_len - p.q_len;

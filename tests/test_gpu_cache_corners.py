@@ -202,3 +202,26 @@ def test_evict_moves_blocks_of_scale_zero(dtype, place, zero):
                                                         dtype), 0) * new[:, None]
             got = raw(now).cpu()[to].view(dtype).double() * new[:, None]
             assert torch.equal(got, exp)
+
+
+# ------------------------------------------------------------------------------ other sizes --
+
+
+@pytest.mark.parametrize("q_len", [1, 12, 300])
+def test_a_table_whose_tokens_pass_31_bits(q_len):
+    """2^23 pages of 256 tokens in a row of the table: its tokens are one more than an int holds."""
+    c = Cache(I8, [700], 4, 2, 256, 32, q_len=q_len, seed=33)
+    before = c.w.clone()
+    want, w = c.run(True), c.w.clone()
+    c.w = before.clone()
+    wide = torch.full((1, 1 << 23), -1, dtype=torch.int32, device=DEV)
+    wide[0, :c.table.shape[1]] = c.table[0]
+    narrow, c.table = c.table, wide
+    out = c.run(True)
+    assert torch.equal(out, want) and torch.equal(c.w, w)
+    c.check(out, before)
+    pools = [[x.clone() for x in (c.k, c.v, c.w, c.ks, c.vs)] for _ in range(2)]
+    got = [api.evict(k, v, w, t, c.len_t, 100, 9, 700, k_scales=ks, v_scales=vs)
+           for (k, v, w, ks, vs), t in zip(pools, (narrow, wide))]
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert all(torch.equal(raw(a).nan_to_num(0), raw(b).nan_to_num(0)) for a, b in zip(*pools))
