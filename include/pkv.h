@@ -407,7 +407,8 @@ PKV_API int paged_attn_q8(const void* q, const void* k_pages, const void* v_page
  *             in flight must not share it.
  * weights_stride : >= max_seq_len.
  * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.
- * H / H_kv is at most 256.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
+ * H / H_kv is at most 256, and max_seq_len at most 8388480 where the prefill kernel
+ * takes the rows.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
  */
 PKV_API size_t paged_attn_weights_workspace_size(int num_seqs, int q_len, int H, int H_kv,
                                                  int max_seq_len, int page_size);

@@ -85,6 +85,9 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
   if (d != 128 || num_seqs > 65535 || H > 65535 || (long long)num_pages * page_size > (1LL << 31))
     return PKV_ERR_UNSUPPORTED;
   if (weights && H / H_kv > 256) return PKV_ERR_UNSUPPORTED;
+  // a grid's second axis: 128-key tiles of the prompt's weights
+  if (weights && !few_rows(num_seqs, q_len, H, H_kv, max_seq_len, true) && max_seq_len > 65535 * 128)
+    return PKV_ERR_UNSUPPORTED;
   const Workspace w = attn_workspace(num_seqs, q_len, H, H_kv, max_seq_len, page_size, weights != nullptr);
   if (w.total() > 0 && (!aligned(workspace, 256) || workspace_bytes < w.total())) return PKV_ERR_WORKSPACE;
 

@@ -862,15 +862,7 @@ void cache_decode_plan(int num_seqs, int H, int H_kv, int max_seq_len, int page_
 cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
   if (p.max_splits > 65535) return cudaErrorNotSupported;           // sequences beyond 2^28 tokens
   const bool w = p.weights != nullptr;
-  cudaError_t e;
-  if (p.cache_dtype == PKV_I8)
-    e = w ? launch_decode<PKV_I8, true>(p, stream) : launch_decode<PKV_I8, false>(p, stream);
-  else if (p.cache_dtype == PKV_E4M3)
-    e = w ? launch_decode<PKV_E4M3, true>(p, stream) : launch_decode<PKV_E4M3, false>(p, stream);
-  else
-    e = w ? launch_decode<PKV_BF16, true>(p, stream) : cudaErrorNotSupported;
-  if (e != cudaSuccess) return e;
-  CacheAttnParams q = p;
+  CacheAttnParams q = p;                            // the finish kernel's
   q.merge_ctas = 0;
   if (p.max_splits > 1) {
     q.merge_warps = 1;                              // about four splits a warp
@@ -888,8 +880,16 @@ cudaError_t launch_cache_decode(const CacheAttnParams& p, cudaStream_t stream) {
     q.range_tokens = q.token_lanes > 8 ? 128 : 1024 / q.token_lanes;
     ctas += (((long long)p.max_seq_len + q.range_tokens - 1) / q.range_tokens) * p.H_kv * p.num_seqs;
   }
-  if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;
-  return ctas ? launch_after(cache_finish_kernel, dim3((unsigned)ctas), kWeightThreads, q, stream) : cudaSuccess;
+  if (ctas > 0x7fffffffLL) return cudaErrorNotSupported;            // before anything is launched
+  cudaError_t e;
+  if (p.cache_dtype == PKV_I8)
+    e = w ? launch_decode<PKV_I8, true>(p, stream) : launch_decode<PKV_I8, false>(p, stream);
+  else if (p.cache_dtype == PKV_E4M3)
+    e = w ? launch_decode<PKV_E4M3, true>(p, stream) : launch_decode<PKV_E4M3, false>(p, stream);
+  else
+    e = w ? launch_decode<PKV_BF16, true>(p, stream) : cudaErrorNotSupported;
+  if (e != cudaSuccess || ctas == 0) return e;
+  return launch_after(cache_finish_kernel, dim3((unsigned)ctas), kWeightThreads, q, stream);
 }
 
 }  // namespace pkv

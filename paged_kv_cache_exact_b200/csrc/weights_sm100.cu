@@ -379,8 +379,7 @@ cudaError_t launch_weights(const CUtensorMap& tq, const CacheAttnParams& p, cuda
       if (dev >= 0 && dev < 64) done[dev] = true;
     }
   }
-  const long long key_tiles = ((long long)p.max_seq_len + BK - 1) / BK;
-  if (key_tiles > 65535) return cudaErrorNotSupported;
+  const long long key_tiles = ((long long)p.max_seq_len + BK - 1) / BK;      // at most 65535: checked by the host
   const dim3 grid(p.H_kv, (unsigned)key_tiles, p.num_seqs);
   prompt_weights_kernel<kCache><<<grid, kThreads, kSmemBytes, stream>>>(tq, p);
   return cudaGetLastError();
