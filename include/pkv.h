@@ -453,6 +453,13 @@ PKV_API int paged_attn_weights(const void* q, const void* k_pages, const void* v
  *               NaN; a zero scale (rows of zeros) moves like any other.
  * workspace   : >= paged_kv_evict_workspace_size() bytes, 256-byte aligned (NULL
  *               if that size is 0), one for each call in flight.
+ * An 8-bit row loses precision each time that it joins a block of a larger
+ * scale s_new: at most half a step, s_new / 2 for int8 and the larger of 2^-4 of
+ * the value and 2^-10 s_new for e4m3.  A block's scale is inherited, so it does not
+ * shrink when the row that set it has gone: one eviction of many tokens costs
+ * less than one at every step (int8, 16-token blocks, normal rows, budget 256, one
+ * token a step, simulated: a row's mean error 0.8% of its norm at first, 1.3% after
+ * 64 steps, 1.5% after 256; rows of very different sizes lose more).
  * A token whose page is outside the pool is not moved, and a length outside its
  * table is clamped; both are flagged.
  */

@@ -10,7 +10,7 @@ import torch
 from _cache_ref import attend, evict, nearest
 from paged_kv_cache_exact_b200 import api
 from paged_kv_cache_exact_b200 import binding as B
-from test_gpu_cache import BF16, DEV, E4M3, I8, Cache, _errors, clean, pool, raw  # noqa: F401
+from test_gpu_cache import BF16, D, DEV, E4M3, I8, Cache, _errors, clean, pool, raw  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -202,6 +202,59 @@ def test_evict_moves_blocks_of_scale_zero(dtype, place, zero):
                                                         dtype), 0) * new[:, None]
             got = raw(now).cpu()[to].view(dtype).double() * new[:, None]
             assert torch.equal(got, exp)
+
+
+@pytest.mark.parametrize("dtype", [I8, E4M3], ids=["i8", "e4m3"])
+def test_many_evictions_follow_the_rule_and_its_bound(dtype):
+    """A token appended and one evicted, 70 times, in place.  Every step's codes and scales are the rule's to the bit,
+    and a kept row is never further from what was appended than what its moves may have cost: half a step each time
+    that it was rounded anew."""
+    gen = torch.Generator().manual_seed(32)
+    H_kv, ps, budget, recent = 2, 16, 64, 9
+    table = torch.tensor([[3, 1, 4, 0, 2]], dtype=torch.int32)
+    k, ks = pool(dtype, 5, ps, 16, H_kv, gen)
+    k, ks = k.to(DEV), ks.to(DEV)
+    v, vs, table_d = k.clone(), ks.clone(), table.to(DEV)
+    w = torch.rand((1, H_kv, 80), generator=gen).to(DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+
+    def rows(n, h):
+        t = torch.arange(n)
+        codes = raw(k).cpu()[table[0].long()[t // ps], t % ps, h].view(dtype).double()
+        return codes, ks.cpu()[table[0].long()[t // ps], 0, h].double()
+
+    new = torch.randn((budget, H_kv, D), generator=gen).to(BF16).to(DEV)
+    api.append_q8(new, new, i32(0, budget), i32(0), table_d, k, v, ks, vs)
+    first, slack = {}, {}
+    for h in range(H_kv):
+        c, s = rows(budget, h)
+        first[h], slack[h] = c * s[:, None], torch.zeros((budget, D), dtype=torch.float64)
+    for step in range(70):
+        old = {h: rows(budget, h) for h in range(H_kv)}
+        new = (torch.randn((1, H_kv, D), generator=gen) * (0.5 + step % 4)).to(BF16).to(DEV)
+        api.append_q8(new, new, i32(0, 1), i32(budget), table_d, k, v, ks, vs)
+        held = {h: rows(budget + 1, h) for h in range(H_kv)}
+        w[0, :, budget] = torch.rand(H_kv, generator=gen).to(DEV)
+        want = evict(w.cpu(), [budget + 1], budget, recent)
+        kept, _ = api.evict(k, v, w, table_d, i32(budget + 1), budget, recent, budget + 1, k_scales=ks, v_scales=vs)
+        for h in range(H_kv):
+            assert kept[0, h].tolist() == want[0][h]
+            i = torch.tensor(want[0][h])
+            c, s = held[h][0][i], held[h][1][i]
+            assert torch.equal(held[h][0][:budget], old[h][0])       # the new row has a block of its own
+            s_new = s.view(-1, 16).amax(-1).repeat_interleave(16)
+            exp = nearest(c * s[:, None] / s_new[:, None], dtype)
+            got, got_s = rows(budget, h)
+            assert torch.equal(got_s, s_new) and torch.equal(got, exp)
+            was = torch.cat([first[h], held[h][0][budget:] * held[h][1][budget:, None]])[i]
+            lost = torch.cat([slack[h], torch.zeros((1, D), dtype=torch.float64)])[i]
+            # half a step: s / 2 for int8; 2^-4 of the value or 2^-10 s for e4m3
+            half = (0.5 * s_new[:, None]).expand(-1, D) if dtype == I8 else \
+                torch.maximum(2.0 ** -4 * (c * s[:, None]).abs(), 2.0 ** -10 * s_new[:, None])
+            lost = lost + torch.where((s_new > s)[:, None], half, 0)
+            assert ((got * got_s[:, None] - was).abs() <= lost * (1 + 1e-9)).all()
+            first[h], slack[h] = was, lost
+    assert torch.equal(raw(k), raw(v)) and torch.equal(ks, vs)
 
 
 # ------------------------------------------------------------------------------ other sizes --
