@@ -333,7 +333,8 @@ PKV_API int paged_kv_copy_pages(void* k_pages, void* v_pages, const int32_t* src
  * writes the block's first token (a reused page needs no clearing), else the
  * block's scale so far, and its old rows are those before the call's first.  So
  * no value is ever clipped, and codes change only where a scale grows.  A block
- * that takes in a NaN or an infinity gets scale NaN and codes 0, and stays NaN
+ * that takes in a NaN or an infinity gets scale NaN, with codes 0 for the call's
+ * rows (older rows keep theirs, which stand for NaN now as well), and stays NaN
  * until its first token is written anew: rows that see the block get NaN from
  * attention over it, others do not.  The weights that a row gives (below) become
  * NaN with a block of K, and do not depend on V.
@@ -369,6 +370,10 @@ PKV_API int paged_kv_copy_pages_q8(void* k_pages, void* v_pages, void* k_scales,
  * A few query rows (what a verifying step has: q_len up to 16, and more where
  * that leaves most of the GPU idle) run on the split kernel of the single-token
  * case, more of them on the prefill kernel; the choice depends on the sizes alone.
+ * Rounding: scores and sums are float32 and out is rounded once; P is rounded for
+ * the product with V: by the split kernel to f16, or over a bf16 cache to two bf16
+ * parts (off by at most 2^-11 of sum P |V|), by the prefill kernel, with its value
+ * scale, to bf16 (2^-8 of it, as in paged_attn).
  * workspace : device scratch of >= paged_attn_q8_workspace_size() bytes, 256-byte
  *             aligned (NULL if that size is 0), one for each call in flight.
  * Codes of live tokens are finite: an e4m3 NaN code (0x7f, 0xff) never comes from
@@ -406,7 +411,9 @@ PKV_API int paged_attn_q8(const void* q, const void* k_pages, const void* v_page
  * weights   : device float32 [num_seqs, H_kv, weights_stride], added to.  Two calls
  *             in flight must not share it.
  * weights_stride : >= max_seq_len.
- * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.
+ * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.  With a
+ *             few rows it holds their scores, 4 num_seqs H q_len max_seq_len bytes:
+ *             a batch with one long sequence is better cut into two calls.
  * H / H_kv is at most 256, and max_seq_len at most 8388480 where the prefill kernel
  * takes the rows.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
  */

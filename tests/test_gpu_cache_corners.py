@@ -79,6 +79,41 @@ def test_results_of_another_stream_outlive_their_name():
     assert torch.equal(copy, want)
 
 
+@pytest.mark.parametrize("form", ["stream", "address", "default stream"])
+def test_a_stream_by_name_or_address(form):
+    c = Cache(E4M3, [900, 31], 16, 2, 16, 16, seed=11)
+    before = c.w.clone()
+    want, w = c.run(True), c.w.clone()
+    c.w.copy_(before)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = c.run(True, stream={"stream": s, "address": s.cuda_stream, "default stream": 0}[form])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(c.w, w)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+@pytest.mark.parametrize("address", [False, True], ids=["stream", "address"])
+def test_captured_with_a_stream_and_what_the_call_allocates(address):
+    """Outputs and workspaces of a captured call come from the graph's memory; two replays on other work's heels."""
+    c = Cache(I8, [700, 40, 1300], 16, 2, 16, 16, seed=12)
+    before = c.w.clone()
+    want, w = c.run(True), c.w.clone()
+    c.w.copy_(before)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = c.run(True, stream=s.cuda_stream if address else s)
+    for _ in range(2):
+        c.w.copy_(before)
+        junk = [torch.full((1 << k,), 3.0, device=DEV) for k in range(8, 22)]
+        g.replay()
+        del junk
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(c.w, w)
+
+
 # ------------------------------------------------------------------- values that are not finite --
 
 
@@ -278,3 +313,23 @@ def test_a_table_whose_tokens_pass_31_bits(q_len):
            for (k, v, w, ks, vs), t in zip(pools, (narrow, wide))]
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert all(torch.equal(raw(a).nan_to_num(0), raw(b).nan_to_num(0)) for a, b in zip(*pools))
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("q_len,lens,H,H_kv,ps,bt", [
+    (2, [700, 2, 3, 4100], 8, 8, 16, 16),
+    (3, [3, 257, 1030], 15, 3, 32, 32),
+    (16, [16, 17, 900], 32, 2, 256, 64),          # 256 rows a kv head
+    (7, [300], 2, 1, 16, 16),
+])
+def test_few_rows_round_the_weights_to_eleven_bits(dtype, q_len, lens, H, H_kv, ps, bt, causal):
+    """Up to 16 rows a head and 256 a kv head go through the single-token kernel, whose P has 11 bits or more:
+    2^-11 of sum p |v|, where the prefill kernel's bf16 P is off by up to 2^-8."""
+    c = Cache(dtype, lens, H, H_kv, ps, bt, q_len=q_len, seed=60 + q_len, q_mul=2.0)
+    want, _, spread, size = attend(c.q, c.k, c.v, c.ks, c.vs, c.table, lens, causal, c.scale)
+    rel = math.expm1(2 * 128 * 2.0 ** -24 * size) + 2.0 ** -20
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + rel) * 1.01 * spread + 1e-30
+    for weights in (False, True)[dtype == BF16:]:
+        err = (c.run(weights, causal=causal).double() - want).abs()
+        assert (err <= tol).all(), f"{float((err / tol).max()):.2f} of the bound"
