@@ -115,7 +115,7 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
   p.num_pages = num_pages, p.max_pages = max_pages_per_seq, p.max_seq_len = max_seq_len;
   p.logit_tokens = max_seq_len;
   p.cache_dtype = cache_dtype, p.causal = causal;
-  p.scale = scale, p.scale_log2 = scale * pkv::kLog2e;
+  p.scale_log2 = scale * pkv::kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few_rows(num_seqs, q_len, H, H_kv, max_seq_len, weights != nullptr)) {
     p.H = H * q_len;

@@ -52,7 +52,7 @@ struct CacheAttnParams {
   int split_tokens, max_splits, weights_stride, logit_tokens, lse_stride;
   int merge_ctas, merge_warps, token_lanes, range_tokens;   // set by the launcher
   int cache_dtype, causal;
-  float scale, scale_log2;     // scale_log2 = scale * log2(e)
+  float scale_log2;            // scale * log2(e)
 };
 
 struct EvictParams {

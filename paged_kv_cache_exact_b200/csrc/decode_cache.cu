@@ -8,8 +8,9 @@
 // per token and kv head, plus 8 bytes of scales per block.  So every K/V row
 // is read once for all query heads of its kv head.  Each of a CTA's four warps
 // takes chunks of 16 tokens of its own (two at a time of an 8-bit cache) through a
-// two-step cp.async ring: 8 KB a warp and 96 KB an SM are on their way while as
-// much is worked on, and no barrier joins the warps before the end.
+// two-step cp.async ring: 8 KB a warp (96 KB an SM of three CTAs, 64 KB of two where
+// a kv head has more than 8 rows) are on their way while as much is worked on, and no
+// barrier joins the warps before the end.
 //
 // Products.  With up to 8 query heads per kv head (16 in two tiles) scores and
 // outputs are small matrix products, written transposed so that the long axis

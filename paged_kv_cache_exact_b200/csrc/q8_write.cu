@@ -10,13 +10,13 @@
 //     code(new rows)  = RNE(x / s_new)
 //     code(old rows)  = RNE(code * s_old / s_new)  where s_new > s_old
 //
-// so a block never clips.  Quotients are rounded exactly (q8.cuh): the result
+// so a block never clips.  (s_new NaN: codes 0 for the new rows, the old ones stay.)  Quotients are rounded exactly (q8.cuh): the result
 // does not depend on how a prompt was cut into calls other than through the
 // definition above.
 //
 // One CTA per (block of the call, a few of the 2 H_kv (head, K or V) pairs): a warp
 // takes 16 of a pair's rows, so a 16-token block has 8 pairs a CTA and a 128-token
-// block one.  Lane i holds elements 4i .. 4i+3 of a row, so a row of new values is
+// block one; a 256-token block has one as well, 32 rows a warp.  Lane i holds elements 4i .. 4i+3 of a row, so a row of new values is
 // one 256-byte load and its codes one 128-byte store.  The rows are read twice,
 // the second time from L1, four at a time: with 16 in registers the rounding is 16
 // copies of its code, which cost a decode step's single row 2 us of instruction
@@ -33,7 +33,7 @@ namespace {
 constexpr int D = 128;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kWarpRows = 16;        // rows of a block that a warp takes
+constexpr int kWarpRows = 16;        // rows of a block that a warp takes (of 256 tokens: 32)
 constexpr int kBatch = 4;            // rows it loads at once
 
 // Four consecutive elements of a new row as stored (bf16 or f32).
