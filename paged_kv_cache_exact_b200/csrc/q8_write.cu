@@ -21,7 +21,7 @@
 // the second time from L1, four at a time: with 16 in registers the rounding is 16
 // copies of its code, which cost a decode step's single row 2 us of instruction
 // fetches (6.2 against 4.2 us) and gained a prompt nothing.  What bounds a prompt
-// is the rounding's instructions, 29 a code on 61% of the issue slots (78 us for
+// is the rounding's instructions, some 31 a code on 67% of the issue slots (78 us for
 // 30027 rows of 8 heads); the floor of 2 bytes read and 1 written per element is
 // 28 us.
 #include "cache_attn.cuh"
