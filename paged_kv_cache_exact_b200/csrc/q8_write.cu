@@ -71,9 +71,9 @@ template <> struct Row4<float> {
 // rows can touch: n rows touch at most floor(n / block) + 2 blocks.
 template <int kCache, typename T>
 __global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const AppendQ8Params p) {
-  __shared__ int s_row0, s_rows, s_off, s_dst;
+  __shared__ int s_row0, s_rows, s_off, s_dst, s_taken;
   __shared__ uint32_t s_max[kWarps];
-  if (threadIdx.x == 0) s_rows = 0;
+  if (threadIdx.x == 0) s_rows = s_taken = 0;
   __syncthreads();
   // The thread whose sequence has this item looks the block up: a search by one
   // thread would be a chain of dependent loads.
@@ -81,6 +81,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_q8_kernel(const AppendQ8Pa
   for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
     const int c0 = p.cu_new[s], c1 = p.cu_new[s + 1];
     if (item < (c0 >> p.block_shift) + 2 * s || item >= (c1 >> p.block_shift) + 2 * s + 2) continue;
+    // One sequence has the item if cu_new never falls; if it does, the first to get
+    // here keeps what the others would otherwise overwrite part by part.
+    if (atomicExch(&s_taken, 1)) break;
     const int n = c1 - c0;
     const int start = p.start_pos[s];
     const int k = item - ((c0 >> p.block_shift) + 2 * s);        // k-th block of this sequence's rows

@@ -333,3 +333,28 @@ def test_few_rows_round_the_weights_to_eleven_bits(dtype, q_len, lens, H, H_kv, 
     for weights in (False, True)[dtype == BF16:]:
         err = (c.run(weights, causal=causal).double() - want).abs()
         assert (err <= tol).all(), f"{float((err / tol).max()):.2f} of the bound"
+
+
+@pytest.mark.parametrize("cu", [[0, 100, 20, 120], [0, 120, 0, 120], [0, 60, 5, 300], [50, 40, 30, 20], [-7, 20, 10, 120]])
+def test_append_with_row_numbers_that_fall_stays_in_its_pages(cu):
+    """cu_new must not fall.  If it does, which rows are written is open, but nothing outside the tables' pages is,
+    and what is written are new rows: one value to all of them shows as that value or as nothing."""
+    gen = torch.Generator().manual_seed(34)
+    k, ks = pool(I8, 40, 32, 16, 2, gen)
+    v, vs = pool(I8, 40, 32, 16, 2, gen)
+    g = [x.to(DEV) for x in (k, v, ks, vs)]
+    table = torch.arange(4, 28, dtype=torch.int32).view(3, 8)
+    new = torch.ones((120, 2, D), dtype=BF16, device=DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    for _ in range(20):
+        api.append_q8(new, new, i32(cu), i32([0, 16, 32]), table.to(DEV), *g)
+    torch.cuda.synchronize()
+    for x, y in zip((k, v, ks, vs), g):
+        y = y.cpu()
+        assert torch.equal(y[:4], x[:4]) and torch.equal(y[28:], x[28:])
+    for codes, scales, was in ((g[0].cpu(), g[2].cpu(), k), (g[1].cpu(), g[3].cpu(), v)):
+        value = codes.double() * scales.double().repeat_interleave(16, 1)[..., None]
+        wrote = (codes != was).any(-1)
+        one = ((value - 1).abs() < 1e-6).all(-1)
+        fresh = (scales.repeat_interleave(16, 1) <= 1 / 127 * 1.0001)        # blocks begun in the call
+        assert (one | ~wrote | ~fresh).all()
