@@ -358,3 +358,39 @@ def test_append_with_row_numbers_that_fall_stays_in_its_pages(cu):
         one = ((value - 1).abs() < 1e-6).all(-1)
         fresh = (scales.repeat_interleave(16, 1) <= 1 / 127 * 1.0001)        # blocks begun in the call
         assert (one | ~wrote | ~fresh).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, I8, E4M3], ids=["bf16", "i8", "e4m3"])
+def test_pages_beyond_32_bits(dtype):
+    """A pool of more than 2^32 bytes whose sequences lie at its end, against the same pages in a small one: append,
+    attention of one, a few and many rows with weights, page copies and eviction, to the bit."""
+    H, H_kv, ps, lens, budget = 16, 8, 64, [900, 300], 200
+    far = (1 << 32) // (ps * H_kv * D * (2 if dtype == BF16 else 1)) + 5
+
+    def run(base):
+        c = Cache(dtype, lens, H, H_kv, ps, 32, seed=35)
+        n = c.k.shape[0]
+        if base:
+            for name in ("k", "v", "ks", "vs"):
+                x = getattr(c, name)
+                if x is not None:
+                    big = torch.empty((base + n, *x.shape[1:]), dtype=x.dtype, device=DEV)
+                    raw(big)[base:] = raw(x)
+                    setattr(c, name, big)
+            c.table = torch.where(c.table >= 0, c.table + base, -1).to(torch.int32)
+        out = []
+        gen = torch.Generator().manual_seed(36)
+        i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+        new = torch.randn((7, H_kv, D), generator=gen).to(BF16).to(DEV)
+        if dtype != BF16:
+            api.append_q8(new, new, i32(0, 3, 7), i32(897, 296), c.table, c.k, c.v, c.ks, c.vs)
+            api.copy_pages_q8(c.k, c.v, c.ks, c.vs, c.table[:1, 1].contiguous(), c.table[1:, 2].contiguous())
+        for q_len in (1, 5, 200):
+            c.q = torch.randn((2, H, q_len, D), generator=gen).to(BF16).to(DEV)
+            out.append(c.run(True))
+        kept, new_lens = api.evict(c.k, c.v, c.w, c.table, c.len_t, budget, 20, 900, k_scales=c.ks, v_scales=c.vs)
+        out += [kept, new_lens, c.w] + [x[base:].view(torch.uint8) for x in (c.k, c.v)]           # dead slots hold NaN
+        return out + [x[base:].nan_to_num(-1) for x in (c.ks, c.vs) if x is not None]
+
+    small, large = run(0), run(far)
+    assert all(torch.equal(a, b) for a, b in zip(small, large)) and torch.isfinite(small[2]).all()
