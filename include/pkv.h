@@ -414,6 +414,8 @@ PKV_API int paged_attn_q8(const void* q, const void* k_pages, const void* v_page
  * workspace : >= paged_attn_weights_workspace_size() bytes, 256-byte aligned.  With a
  *             few rows it holds their scores, 4 num_seqs H q_len max_seq_len bytes:
  *             a batch with one long sequence is better cut into two calls.
+ * Where the prefill kernel takes the rows, out must not overlap q (PKV_ERR_INVALID_ARG):
+ * q is read again for the weights once out is written.
  * H / H_kv is at most 256, and max_seq_len at most 8388480 where the prefill kernel
  * takes the rows.  A PKV_F32 cache is PKV_ERR_UNSUPPORTED.
  */

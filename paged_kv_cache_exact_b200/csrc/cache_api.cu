@@ -90,6 +90,11 @@ int run_attn(const void* q, const void* k_pages, const void* v_pages, const void
     return PKV_ERR_UNSUPPORTED;
   const Workspace w = attn_workspace(num_seqs, q_len, H, H_kv, max_seq_len, page_size, weights != nullptr);
   if (w.total() > 0 && (!aligned(workspace, 256) || workspace_bytes < w.total())) return PKV_ERR_WORKSPACE;
+  if (weights && !few_rows(num_seqs, q_len, H, H_kv, max_seq_len, true)) {    // q is read again once out is written
+    const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t bytes = (uintptr_t)num_seqs * H * q_len * d * sizeof(__nv_bfloat16);
+    if (a < b + bytes && b < a + bytes) return PKV_ERR_INVALID_ARG;
+  }
 
   pkv::CacheAttnParams p{};
   if (int r = pkv::device_error_word(&p.err)) return r;

@@ -22,6 +22,14 @@ def test_a_prompts_weights_over_too_many_keys_are_refused_before_the_attention_r
     assert _call("paged_attn_weights", ATTN + W_TAIL[0], ATTN_OK + W_TAIL[1], kw) == B.PKV_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("q_len,off", [(300, 0), (300, 2 * 8 * 300 * 256 - 16), (300, -16), (17, 0)])
+def test_prompt_weights_with_an_output_over_q_are_refused(q_len, off):
+    """A prompt's weights read q again after out is written."""
+    q = 1 << 24
+    kw = dict(q=q, out=q + off, q_len=q_len)
+    assert _call("paged_attn_weights", ATTN + W_TAIL[0], ATTN_OK + W_TAIL[1], kw) == B.PKV_ERR_INVALID_ARG
+
+
 # -------------------------------------------------------- the tensor-level functions' own checks --
 
 

@@ -394,3 +394,22 @@ def test_pages_beyond_32_bits(dtype):
 
     small, large = run(0), run(far)
     assert all(torch.equal(a, b) for a, b in zip(small, large)) and torch.isfinite(small[2]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, I8], ids=["bf16", "i8"])
+@pytest.mark.parametrize("q_len", [1, 6, 100])
+def test_an_output_in_the_place_of_q(dtype, q_len):
+    """A few rows may be written over their queries (several splits, several CTAs a kv head); a prompt with weights
+    is refused, as its queries are read again."""
+    c = Cache(dtype, [1500, 130], 24, 2, 16, 16, q_len=q_len, seed=37)
+    before = c.w.clone()
+    want, w = c.run(True), c.w.clone()
+    c.w = before.clone()
+    if q_len > 16:
+        q = c.q.clone()
+        with pytest.raises(B.PkvError) as e:
+            c.run(True, out=c.q)
+        assert e.value.status == B.PKV_ERR_INVALID_ARG and torch.equal(c.q, q) and torch.equal(c.w, before)
+        return
+    assert c.run(True, out=c.q) is c.q
+    assert torch.equal(c.q, want) and torch.equal(c.w, w)
